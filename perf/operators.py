@@ -5,8 +5,8 @@ it is true. `exact` computes the same results in 64 bits.
 
 The cache's layout (one uint8 tensor [b, kv_heads, capacity / 64, block bytes]): a block holds 64 tokens of one
 key/value head, as [K codes | K parameters | V codes | V parameters]. Each token's row of codes has dh / 2 bytes: a
-32-bit word holds 8 consecutive dimensions (dimension 8u + i in bits 4i .. 4i + 3 of word u), and the words of a row are
-permuted (`_word_order`). The parameters are two bf16, scale then minimum, per token and 64 dimensions; a code c stands
+32-bit word holds 8 consecutive dimensions (dimension 8u + i in bits 4i .. 4i + 3 of word u; the words of K are rotated
+left by 3 bits), and the words of a row are permuted (`_word_order`). The parameters are two bf16, scale then minimum, per token and 64 dimensions; a code c stands
 for minimum + scale c.
 """
 
@@ -52,12 +52,19 @@ def _quantise(x):
     return codes, scale, low
 
 
+def _rotate(words, by):
+    """32-bit words rotated left by `by` bits."""
+    return (words << by) | ((words >> (32 - by)) & ((1 << by) - 1))
+
+
 def _pack(x, which):
     """Code bytes [..., blocks, 32 dh] and parameter bytes of x [..., capacity, dh] (capacity a multiple of 64)."""
     dh = x.shape[-1]
     codes, scale, low = _quantise(x)
     codes = codes.to(torch.uint8).flatten(-2)
     data = codes[..., 0::2] | (codes[..., 1::2] << 4)
+    if which == "k":
+        data = _rotate(data.view(torch.int32), 3).view(torch.uint8)
     data = data.unflatten(-1, (dh // 8, 4)).unflatten(-3, (-1, BLOCK))
     order = _word_order(dh, which, x.device)[..., None].expand(data.shape)
     data = torch.gather(data, -2, order)
@@ -72,6 +79,8 @@ def _unpack(data, dh, which):
     words = data[..., at:params].unflatten(-1, (BLOCK, dh // 8, 4))
     back = torch.argsort(_word_order(dh, which, data.device), -1)[..., None].expand(words.shape)
     words = torch.gather(words, -2, back)
+    if which == "k":
+        words = _rotate(words.view(torch.int32), 29).view(torch.uint8)
     codes = torch.stack((words & 15, words >> 4), -1).flatten(-3).float().unflatten(-1, (-1, GROUP))
     pair = data[..., params:stop].unflatten(-1, (BLOCK, dh // GROUP, 4)).contiguous().view(torch.bfloat16).float()
     return (pair[..., 1:] + pair[..., :1] * codes).flatten(-2).flatten(2, 3)
@@ -401,9 +410,10 @@ def _exact_rows(data, dh, which):
         place, first = u, _sections(dh)[2]
     else:
         place, first = ((u % 8) ^ (4 * ((row // 2) % 2))) * 2 + u // 8, _sections(dh)[2]
-    byte = (first + row * (dh // 2) + place * 4 + (dim % 8) // 2).to(data.device)
-    shift = (4 * (dim % 2)).to(data.device)
-    code = ((data[..., byte.flatten()] >> shift.flatten().to(torch.uint8)) & 15).view(h, blocks, BLOCK, dh)
+    byte = (first + row * (dh // 2) + place * 4).to(data.device)  # of the dimension's word
+    word = sum(data[..., (byte + i).flatten()].long() << (8 * i) for i in range(4))
+    shift = (4 * (dim % 8) + (3 if which == "k" else 0)).to(data.device).flatten()
+    code = (((word | (word << 32)) >> shift) & 15).view(h, blocks, BLOCK, dh)
     at = first + BLOCK * dh // 2
     par = (at + (row * (dh // GROUP) + dim // GROUP) * 4).to(data.device)
 
