@@ -32,6 +32,8 @@ EXPORTED = (
     "bpt_qkv_projection", "bpt_attention", "bpt_ffn_backward_workspace_bytes", "bpt_ffn_backward",
     "bpt_attention_lse", "bpt_attention_backward_workspace_bytes", "bpt_attention_backward",
     "bpt_layer_backward_workspace_bytes", "bpt_layer_backward", "bpt_layer_forward_save", "bpt_layer_backward_saved",
+    "bpt_rotary_frequencies", "bpt_rotary", "bpt_kv4_cache_bytes", "bpt_kv4_store", "bpt_kv4_load",
+    "bpt_kv4_attention_workspace_bytes", "bpt_kv4_attention", "bpt_kv4_evict",
     "bpt_stream_status", "bpt_device_status", "bpt_wait_flag",
     "bpt_launch_count", "bpt_set_kernel_timing", "bpt_kernel_times",
 )
@@ -100,6 +102,24 @@ def lib() -> ctypes.CDLL:
     L.bpt_layer_forward_save.argtypes = [vp] * 9 + [i] * 8 + [vp] * 4
     L.bpt_layer_backward_saved.restype = i
     L.bpt_layer_backward_saved.argtypes = [vp] * 12 + [i] * 6 + [vp] * 10 + [sz, vp]
+    d = ctypes.c_double
+    L.bpt_rotary_frequencies.restype = i
+    L.bpt_rotary_frequencies.argtypes = [i, d, i, d, i, d, d, vp, ctypes.POINTER(ctypes.c_float)]
+    L.bpt_rotary.restype = i
+    L.bpt_rotary.argtypes = ([i, vp, ll, ll, vp, ll, ll] + [i] * 7 + [vp, ctypes.c_float, vp, i, ll, ll, i]
+                             + [vp, ll, ll] * 2 + [vp])
+    L.bpt_kv4_cache_bytes.restype = sz
+    L.bpt_kv4_cache_bytes.argtypes = [i] * 4
+    L.bpt_kv4_store.restype = i
+    L.bpt_kv4_store.argtypes = [vp] + [i] * 4 + [vp, ll, ll] * 2 + [i, vp, vp, vp]
+    L.bpt_kv4_load.restype = i
+    L.bpt_kv4_load.argtypes = [vp] + [i] * 4 + [vp, vp, i, vp, vp, vp]
+    L.bpt_kv4_attention_workspace_bytes.restype = sz
+    L.bpt_kv4_attention_workspace_bytes.argtypes = [i] * 7
+    L.bpt_kv4_attention.restype = i
+    L.bpt_kv4_attention.argtypes = [vp, ll, ll, vp, vp] + [i] * 7 + [vp] * 4 + [sz, vp]
+    L.bpt_kv4_evict.restype = i
+    L.bpt_kv4_evict.argtypes = [vp] * 3 + [i] * 6 + [vp, i] + [vp] * 4
     L.bpt_stream_status.restype = i
     L.bpt_stream_status.argtypes = [vp]
     L.bpt_device_status.restype = i
@@ -422,6 +442,244 @@ def ffn_backward(hid: torch.Tensor, W1: torch.Tensor, b1: torch.Tensor, W2: torc
                                _ptr(ws), ws.numel(), _stream(stream))
     _check(r, "bpt_ffn_backward")
     return g
+
+
+# how a long context scales the angles of rotary positions: include/bpt.h
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                       original: int = 0, low_turns: float = 1.0, high_turns: float = 32.0):
+    """Radians per position of the rot / 2 pairs of a head (fp64, host memory)
+    and the magnitude that goes with them (bpt_rotary_frequencies), for
+    `rotary`. scaling: "plain", "linear", "base" or "ramp" (a context `factor`
+    times as long; "ramp" also needs the original length in tokens)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {tuple(ROTARY_SCALINGS)}")
+    freq = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    magnitude = ctypes.c_float()
+    _check(lib().bpt_rotary_frequencies(int(rot), float(base), ROTARY_SCALINGS[scaling], float(factor), int(original),
+                                        float(low_turns), float(high_turns), freq.data_ptr(),
+                                        ctypes.byref(magnitude)), "bpt_rotary_frequencies")
+    return freq, magnitude.value
+
+
+def _rows(t: torch.Tensor, name: str, width: int, dtypes, like: Optional[torch.Tensor] = None) -> tuple:
+    """(pointer, elements between sequences, elements between tokens) of a CUDA
+    tensor [b, s, width] whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != width:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [b, s, {width}]")
+    if like is not None and (t.shape[:2] != like.shape[:2] or t.device != like.device or t.dtype != like.dtype):
+        raise ValueError(f"{name} must have the tokens, dtype and device of the first tensor")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+class _On:
+    """The tensors' device and the given stream (default: the device's current
+    one) as torch's current ones, so that outputs and workspaces belong to the
+    stream that uses them. Enters as the stream's handle."""
+
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        self.device, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.device)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return (self.stream if self.stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *exc) -> None:
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], heads: int, kv_heads: int, inv_freq: torch.Tensor,
+           positions: Optional[torch.Tensor] = None, offset: int = 0, interleaved: bool = False,
+           magnitude: float = 1.0, inverse: bool = False, q_out: Optional[torch.Tensor] = None,
+           k_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Rotary positions of q [b, s, heads * dh] and k [b, s, kv_heads * dh] or
+    None (bf16 or fp32, rows contiguous, any strides between them), in one
+    launch (bpt_rotary). inv_freq (fp64, host memory) and magnitude are
+    rotary_frequencies'; 2 * len(inv_freq) dimensions of each head are turned.
+    positions: int32 or int64, [b, s] or [s], or None: token t is at offset +
+    t. inverse=True is the gradient: dq, dk of the turned q, k in, of q, k out.
+    q_out and k_out may be q and k themselves. Returns (q_out, k_out)."""
+    b, s = q.shape[:2]
+    if heads <= 0 or q.shape[-1] % heads:
+        raise ValueError(f"q's last dimension {q.shape[-1]} does not hold {heads} heads")
+    dh = q.shape[-1] // heads
+    kinds = (torch.bfloat16, torch.float32)
+    pq = _rows(q, "q", heads * dh, kinds)
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous fp64 vector in host memory")
+    pk = pko = (None, 0, 0)
+    if k is None:
+        kv_heads, k_out = 0, None
+    else:
+        pk = _rows(k, "k", kv_heads * dh, kinds, q)
+    at, size, step = None, 8, 0
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64) or positions.device != q.device:
+            raise TypeError("positions must be int32 or int64 on q's device")
+        if tuple(positions.shape) not in ((b, s), (s,)):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(b, s)} or {(s,)}")
+        if positions.stride(-1) != 1 and s > 1:
+            raise ValueError("positions must be contiguous along the sequence")
+        at, size = positions.data_ptr(), positions.element_size()
+        step = positions.stride(0) if positions.dim() == 2 else 0
+    dtype = BPT_DTYPE_F32 if q.dtype == torch.float32 else BPT_DTYPE_BF16
+    with _On(q.device, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((b, s, heads * dh), dtype=q.dtype, device=q.device)
+        pqo = _rows(q_out, "q_out", heads * dh, kinds, q)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty((b, s, kv_heads * dh), dtype=q.dtype, device=q.device)
+            pko = _rows(k_out, "k_out", kv_heads * dh, kinds, q)
+        r = lib().bpt_rotary(dtype, *pq, *pk, b, s, heads, kv_heads, dh, 2 * inv_freq.numel(), int(bool(interleaved)),
+                             inv_freq.data_ptr(), float(magnitude), at, size, step, int(offset), int(bool(inverse)),
+                             *pqo, *pko, st)
+    _check(r, "bpt_rotary")
+    return q_out, k_out
+
+
+class KV4Cache:
+    """A key/value cache in 4 bits over `data`, a contiguous uint8 CUDA tensor
+    [b, kv_heads, capacity / 64, block bytes] (9216 bytes for dh = 128, 4608
+    for 64; include/bpt.h). kv4_cache() makes an empty one."""
+
+    __slots__ = ("data", "b", "kv_heads", "capacity", "dh")
+
+    def __init__(self, data: torch.Tensor, dh: int):
+        block = {64: 4608, 128: 9216}.get(dh)
+        if block is None:
+            raise ValueError("dh must be 64 or 128")
+        if data.dtype != torch.uint8 or not data.is_cuda or not data.is_contiguous():
+            raise TypeError("data must be a contiguous uint8 CUDA tensor")
+        if data.dim() != 4 or data.shape[3] != block:
+            raise ValueError(f"data has shape {tuple(data.shape)}, expected [b, kv_heads, capacity / 64, {block}]")
+        self.data, self.dh = data, dh
+        self.b, self.kv_heads, self.capacity = data.shape[0], data.shape[1], data.shape[2] * 64
+
+    def _args(self) -> tuple:
+        return self.data.data_ptr(), self.b, self.kv_heads, self.capacity, self.dh
+
+    def _ints(self, t: torch.Tensor, name: str) -> int:
+        if t.dtype != torch.int32 or t.device != self.data.device or tuple(t.shape) != (self.b,) \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor [{self.b}] on the cache's device")
+        return t.data_ptr()
+
+    def _floats(self, t: torch.Tensor, name: str) -> int:
+        shape = (self.b, self.kv_heads, self.capacity)
+        if t.dtype != torch.float32 or t.device != self.data.device or tuple(t.shape) != shape \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp32 tensor {shape} on the cache's device")
+        return t.data_ptr()
+
+
+def kv4_cache(b: int, kv_heads: int, capacity: int, dh: int, device="cuda") -> KV4Cache:
+    """An empty 4-bit cache of b sequences of `capacity` tokens (rounded up to a
+    multiple of 64)."""
+    blocks = (int(capacity) + 63) // 64
+    nbytes = int(lib().bpt_kv4_cache_bytes(b, kv_heads, blocks * 64, dh))
+    if nbytes == 0:
+        raise ValueError(f"no cache of b={b}, kv_heads={kv_heads}, capacity={capacity}, dh={dh}")
+    data = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    return KV4Cache(data.view(b, kv_heads, blocks, -1), dh)
+
+
+def kv4_store(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor,
+              counts: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Store tokens (bf16 [b, n, kv_heads * dh], rows contiguous) at places
+    start[beta] .. of each sequence, the first counts[beta] of them (default:
+    all n); start and counts int32 [b] (bpt_kv4_store)."""
+    width = cache.kv_heads * cache.dh
+    pk = _rows(k, "k", width, (torch.bfloat16,))
+    pv = _rows(v, "v", width, (torch.bfloat16,), k)
+    if k.shape[0] != cache.b or k.device != cache.data.device:
+        raise ValueError(f"k must hold {cache.b} sequences on the cache's device")
+    ps = cache._ints(start, "start")
+    pc = None if counts is None else cache._ints(counts, "counts")
+    with _On(k.device, stream) as st:
+        r = lib().bpt_kv4_store(*cache._args(), *pk, *pv, k.shape[1], ps, pc, st)
+    _check(r, "bpt_kv4_store")
+
+
+def kv4_load(cache: KV4Cache, lens: torch.Tensor, n: int, start: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """The values at places start[beta] .. start[beta] + n - 1 (default: from 0)
+    of each sequence, as bf16 k, v [b, n, kv_heads * dh]; zeros at or past
+    lens[beta] (bpt_kv4_load)."""
+    pl = cache._ints(lens, "lens")
+    ps = None if start is None else cache._ints(start, "start")
+    dev = cache.data.device
+    with _On(dev, stream) as st:
+        k, v = torch.empty((2, cache.b, n, cache.kv_heads * cache.dh), dtype=torch.bfloat16, device=dev)
+        r = lib().bpt_kv4_load(*cache._args(), ps, pl, n, k.data_ptr(), v.data_ptr(), st)
+    _check(r, "bpt_kv4_load")
+    return k, v
+
+
+def kv4_attention(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, heads: int, causal: bool = True,
+                  weights: Optional[torch.Tensor] = None, return_lse: bool = False,
+                  stream: Optional[torch.cuda.Stream] = None):
+    """Attention of the n newest tokens of each sequence, q [b, n, heads * dh]
+    (bf16, rows contiguous), over its lens[beta] cached tokens, the new ones
+    among them (bpt_kv4_attention). weights: fp32 [b, kv_heads, capacity], to
+    which every cached token's softmax weight is added. Returns o (bf16 [b, n,
+    heads * dh]), with return_lse (o, lse2 fp32 [b, heads, n])."""
+    pq = _rows(q, "q", heads * cache.dh, (torch.bfloat16,))
+    if q.shape[0] != cache.b or q.device != cache.data.device:
+        raise ValueError(f"q must hold {cache.b} sequences on the cache's device")
+    pl = cache._ints(lens, "lens")
+    pw = None if weights is None else cache._floats(weights, "weights")
+    n, dev = q.shape[1], q.device
+    data, b, kv_heads, capacity, dh = cache._args()
+    nbytes = int(lib().bpt_kv4_attention_workspace_bytes(b, n, heads, kv_heads, capacity, dh, int(pw is not None)))
+    with _On(dev, stream) as st:
+        o = torch.empty((b, n, heads * dh), dtype=torch.bfloat16, device=dev)
+        lse2 = torch.empty((b, heads, n), dtype=torch.float32, device=dev) if return_lse else None
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        r = lib().bpt_kv4_attention(*pq, data, pl, b, n, heads, kv_heads, capacity, dh, int(bool(causal)),
+                                    o.data_ptr(), None if lse2 is None else lse2.data_ptr(), pw, ws.data_ptr(),
+                                    ws.numel(), st)
+    _check(r, "bpt_kv4_attention")
+    return (o, lse2) if return_lse else o
+
+
+def kv4_evict(cache: KV4Cache, weights: torch.Tensor, lens: torch.Tensor, keep: int, recent: int, out: KV4Cache,
+              stream: Optional[torch.cuda.Stream] = None):
+    """Move each head's `recent` newest and heaviest other tokens, `keep` in all,
+    to the cache `out` (bpt_kv4_evict). weights: fp32 [b, kv_heads, capacity]
+    as kv4_attention accumulates them. Returns (kept int32 [b, kv_heads, keep],
+    -1 past the kept ones; the new lens; the kept tokens' weights, for out)."""
+    dev = cache.data.device
+    if (out.b, out.kv_heads, out.dh) != (cache.b, cache.kv_heads, cache.dh) or out.data.device != dev:
+        raise ValueError("out must have the sequences, heads and device of the cache")
+    pw, pl = cache._floats(weights, "weights"), cache._ints(lens, "lens")
+    data, b, kv_heads, capacity, dh = cache._args()
+    with _On(dev, stream) as st:
+        kept = torch.empty((b, kv_heads, max(int(keep), 0)), dtype=torch.int32, device=dev)
+        new_lens = torch.empty(b, dtype=torch.int32, device=dev)
+        new_weights = torch.empty((b, kv_heads, out.capacity), dtype=torch.float32, device=dev)
+        r = lib().bpt_kv4_evict(data, pw, pl, b, kv_heads, capacity, dh, int(keep), int(recent), out.data.data_ptr(),
+                                out.capacity, new_weights.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), st)
+    _check(r, "bpt_kv4_evict")
+    return kept, new_lens, new_weights
 
 
 def stream_status(stream: Optional[torch.cuda.Stream] = None) -> int:

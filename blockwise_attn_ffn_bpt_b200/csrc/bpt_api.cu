@@ -1696,6 +1696,7 @@ const char* bpt_status_string(int status) {
     case BPT_ERR_TIMEOUT: return "BPT_ERR_TIMEOUT: a kernel gave up a bounded wait";
     case BPT_ERR_UNSUPPORTED: return "BPT_ERR_UNSUPPORTED: the current device is not sm_100";
     case BPT_ERR_DTYPE: return "BPT_ERR_DTYPE: unknown dtype";
+    case BPT_ERR_RANGE: return "BPT_ERR_RANGE: a length, start or count in device memory points outside the cache";
     default: return "unknown bpt status";
   }
 }
@@ -2317,3 +2318,5 @@ int bpt_kernel_times(bpt_kernel_time* out, int max) {
 }
 
 }  // extern "C"
+
+#include "serving_api.cuh"

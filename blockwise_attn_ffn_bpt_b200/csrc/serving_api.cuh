@@ -1,0 +1,430 @@
+// Entry points of rotary positions and of the 4-bit key/value cache: argument
+// checks and launches. Included by bpt_api.cu, whose checks, status words and
+// launch log they share.
+#pragma once
+
+#include "kv4_attention.cuh"
+#include "kv4_cache.cuh"
+#include "kv4_evict.cuh"
+#include "rotary.cuh"
+
+namespace bpt {
+namespace {
+
+// Token rows of one tensor: row (beta, t) at p + beta * bs + t * ld bytes,
+// `width` bytes long.
+struct TokenRows {
+  const void* p;
+  int b, s;
+  long long bs, ld;
+  size_t width;
+  size_t extent() const { return (size_t)((b - 1) * bs + (s - 1) * ld) + width; }
+  Range range() const { return rng(p, extent()); }
+};
+
+// Strides that keep every byte of the tensor within 2^62 of its start.
+bool strides_ok(const TokenRows& r) {
+  const long long most = 1LL << 62;
+  if (r.bs < 0 || r.ld < 0) return false;
+  if (r.b > 1 && r.bs > most / r.b) return false;
+  if (r.s > 1 && r.ld > most / r.s) return false;
+  return r.b * r.bs + r.s * r.ld <= most;
+}
+
+// Whether no two rows of one tensor share a byte (required of outputs).
+bool rows_distinct(const TokenRows& r) {
+  const long long w = (long long)r.width;
+  if (r.s > 1 && r.ld < w) return false;
+  if (r.b > 1 && r.bs < w) return false;
+  if (r.s == 1 || r.b == 1) return true;
+  return r.bs >= (r.s - 1) * r.ld + w || r.ld >= (r.b - 1) * r.bs + w;
+}
+
+// Whether two tensors may share a byte. Rows of one buffer side by side (q, k
+// and v of a fused projection) have the same strides and do not.
+bool rows_overlap(const TokenRows& x, const TokenRows& y) {
+  if (!overlap(x.range(), y.range())) return false;
+  if (x.b != y.b || x.s != y.s || (x.b > 1 && x.bs != y.bs) || (x.s > 1 && x.ld != y.ld)) return true;
+  long long period = 0;  // every row of both starts at a multiple of it from the first one
+  if (x.b == 1)
+    period = x.s == 1 ? 0 : x.ld;
+  else if (x.s == 1)
+    period = x.bs;
+  else if (x.ld > 0 && x.bs % x.ld == 0)
+    period = x.ld;
+  else if (x.bs > 0 && x.ld % x.bs == 0)
+    period = x.bs;
+  if (period <= 0) return true;
+  const long long d = (long long)((reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p)));
+  const long long at = ((d % period) + period) % period;
+  return !(at >= (long long)x.width && at + (long long)y.width <= period);
+}
+
+bool same_rows(const TokenRows& x, const TokenRows& y) {
+  return x.p == y.p && (x.b == 1 || x.bs == y.bs) && (x.s == 1 || x.ld == y.ld);
+}
+
+bool aligned(const TokenRows& r, long long a) {
+  return reinterpret_cast<uintptr_t>(r.p) % a == 0 && (r.b == 1 || r.bs % a == 0) && (r.s == 1 || r.ld % a == 0);
+}
+
+int check_dh(int dh) { return dh == 64 || dh == 128 ? BPT_OK : BPT_ERR_SHAPE; }
+
+size_t kv4_bytes(int b, int kv_heads, int capacity, int dh) {
+  return (size_t)b * kv_heads * (capacity / KV4_BLOCK) * (dh == 128 ? Kv4<128>::BYTES : Kv4<64>::BYTES);
+}
+
+// b sequences of n new tokens (n = 0 where there are none) on a cache
+int check_kv4(int b, int n, int kv_heads, int capacity, int dh) {
+  const long long most = 0x7fffffffLL;
+  if (b < 0 || n < 0 || kv_heads <= 0 || capacity <= 0 || capacity % KV4_BLOCK) return BPT_ERR_SHAPE;
+  BPT_TRY(check_dh(dh));
+  if ((long long)b * kv_heads > most || (long long)b * n > most) return BPT_ERR_SHAPE;
+  if ((long long)n * kv_heads > most / (dh / 8)) return BPT_ERR_SHAPE;
+  if ((double)b * kv_heads * capacity * dh > 4e18) return BPT_ERR_SHAPE;
+  return BPT_OK;
+}
+
+unsigned grid_y(long long rows) { return (unsigned)std::min<long long>(rows, 65535); }
+
+template <typename T, int W>
+void launch_rotary(const RotaryArgs& a, bool interleaved, dim3 grid, cudaStream_t st) {
+  if (interleaved)
+    rotary_kernel<T, W, true><<<grid, ROT_THREADS, 0, st>>>(a);
+  else
+    rotary_kernel<T, W, false><<<grid, ROT_THREADS, 0, st>>>(a);
+}
+
+struct Kv4AttnLayout {
+  size_t lse = 0, scores = 0, total = 0;
+};
+
+Kv4AttnLayout kv4_attn_layout(int b, int n, int heads, int capacity, bool weights) {
+  Kv4AttnLayout l;
+  size_t at = 0;
+  l.lse = at;
+  at += align_up((size_t)b * heads * n * 4, 256);
+  l.scores = at;
+  if (weights) at += align_up((size_t)b * heads * n * capacity * 4, 256);
+  l.total = at;
+  return l;
+}
+
+int check_kv4_attention(int b, int n, int heads, int kv_heads, int capacity, int dh) {
+  BPT_TRY(check_kv4(b, n, kv_heads, capacity, dh));
+  if (heads <= 0 || heads % kv_heads) return BPT_ERR_SHAPE;
+  if ((long long)b * n * heads > 0x7fffffffLL) return BPT_ERR_SHAPE;
+  if ((double)b * n * heads * capacity > 1e18) return BPT_ERR_SHAPE;
+  return BPT_OK;
+}
+
+}  // namespace
+}  // namespace bpt
+
+extern "C" {
+
+int bpt_rotary_frequencies(int rot, double base, int scaling, double factor, int original, double low_turns,
+                           double high_turns, double* inv_freq, float* magnitude) {
+  if (rot < 2 || rot > 2 * ROT_MAX_PAIRS || rot % 2) return BPT_ERR_SHAPE;
+  if (!(base > 0.0) || !std::isfinite(base)) return BPT_ERR_SHAPE;
+  if (scaling < BPT_ROTARY_PLAIN || scaling > BPT_ROTARY_RAMP) return BPT_ERR_SHAPE;
+  if (!(factor >= 1.0) || !std::isfinite(factor)) return BPT_ERR_SHAPE;
+  if (scaling == BPT_ROTARY_BASE && rot == 2) return BPT_ERR_SHAPE;
+  if (scaling == BPT_ROTARY_RAMP && (original <= 0 || !(low_turns < high_turns))) return BPT_ERR_SHAPE;
+  if (!inv_freq || !magnitude) return BPT_ERR_NULL;
+  constexpr double two_pi = 6.283185307179586476925286766559;
+  if (scaling == BPT_ROTARY_BASE) base *= std::pow(factor, (double)rot / (rot - 2));
+  *magnitude = 1.0f;
+  if (scaling == BPT_ROTARY_RAMP) *magnitude = (float)(0.1 * std::log(factor) + 1.0);
+  for (int j = 0; j < rot / 2; ++j) {
+    const double f = std::pow(base, -2.0 * j / rot);
+    double keep = 1.0;  // the share of f that is not divided by the factor
+    if (scaling == BPT_ROTARY_LINEAR) keep = 0.0;
+    if (scaling == BPT_ROTARY_RAMP)
+      keep = std::min(1.0, std::max(0.0, (original * f / two_pi - low_turns) / (high_turns - low_turns)));
+    inv_freq[j] = f * (keep + (1.0 - keep) / factor);
+  }
+  return BPT_OK;
+}
+
+int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const void* k, long long bs_k,
+               long long ld_k, int b, int s, int heads, int kv_heads, int dh, int rot, int interleaved,
+               const double* inv_freq, float magnitude, const void* positions, int position_bytes,
+               long long position_stride, long long offset, int inverse, void* q_out, long long bs_qo,
+               long long ld_qo, void* k_out, long long bs_ko, long long ld_ko, void* stream) {
+  if (dtype != BPT_DTYPE_BF16 && dtype != BPT_DTYPE_F32) return BPT_ERR_DTYPE;
+  if (positions && position_bytes != 4 && position_bytes != 8) return BPT_ERR_DTYPE;
+  if (b < 0 || s < 0 || heads <= 0 || kv_heads < 0) return BPT_ERR_SHAPE;
+  BPT_TRY(check_dh(dh));
+  if (rot < 2 || rot > dh || rot % 2) return BPT_ERR_SHAPE;
+  if ((long long)b * s > 0x7fffffffLL || ((long long)heads + kv_heads) * dh > 0x7fffffffLL / 64) return BPT_ERR_SHAPE;
+  if (position_stride < 0) return BPT_ERR_SHAPE;
+  if ((long long)b * s == 0) return BPT_OK;
+  const bool keys = kv_heads > 0;
+  if (!q || !q_out || !inv_freq || (keys && (!k || !k_out))) return BPT_ERR_NULL;
+  const int es = dtype == BPT_DTYPE_F32 ? 4 : 2;
+  TokenRows in[2] = {{q, b, s, bs_q * es, ld_q * es, (size_t)heads * dh * es},
+                     {k, b, s, bs_k * es, ld_k * es, (size_t)kv_heads * dh * es}};
+  TokenRows out[2] = {{q_out, b, s, bs_qo * es, ld_qo * es, (size_t)heads * dh * es},
+                      {k_out, b, s, bs_ko * es, ld_ko * es, (size_t)kv_heads * dh * es}};
+  const int nt = keys ? 2 : 1;
+  const TokenRows pos{positions, b, s, position_stride * position_bytes, position_bytes, (size_t)position_bytes};
+  if (positions && (!strides_ok(pos) || reinterpret_cast<uintptr_t>(positions) % position_bytes))
+    return strides_ok(pos) ? BPT_ERR_ALIGN : BPT_ERR_SHAPE;
+  bool wide = true, in_place[2] = {false, false};
+  for (int i = 0; i < nt; ++i) {
+    if (!strides_ok(in[i]) || !strides_ok(out[i]) || !rows_distinct(out[i])) return BPT_ERR_SHAPE;
+    if (!aligned(in[i], es) || !aligned(out[i], es)) return BPT_ERR_ALIGN;
+    wide = wide && aligned(in[i], 16) && aligned(out[i], 16);
+    in_place[i] = same_rows(in[i], out[i]);
+  }
+  for (int i = 0; i < nt; ++i) {
+    for (int j = 0; j < nt; ++j)
+      if (!(i == j && in_place[i]) && rows_overlap(out[i], in[j])) return BPT_ERR_ALIAS;
+    if (positions && overlap(out[i].range(), pos.range())) return BPT_ERR_ALIAS;
+  }
+  if (keys && rows_overlap(out[0], out[1])) return BPT_ERR_ALIAS;
+
+  // 16-byte vectors where a vector holds whole pairs' halves of every row;
+  // one pair at a time otherwise
+  const int full = 16 / es;
+  const int w = wide && (rot / 2) % full == 0 ? full : 1;
+  RotaryArgs a{};
+  for (int i = 0; i < nt; ++i)
+    a.t[i] = {in[i].p, const_cast<void*>(out[i].p), in[i].bs / es, in[i].ld / es, out[i].bs / es, out[i].ld / es};
+  a.heads0 = heads;
+  a.heads1 = kv_heads;
+  a.in_place0 = in_place[0];
+  a.in_place1 = in_place[1];
+  a.tokens = b * s;
+  a.s = s;
+  a.dh = dh;
+  a.rot = rot;
+  a.units = (heads + kv_heads) * (dh / (2 * w));
+  a.chunk = std::min(a.units, ROT_THREADS * ROT_UNROLL);
+  a.tile = std::max(1, std::min(ROT_TABLE / (rot / 2), ROT_THREADS * ROT_UNROLL / a.units));
+  a.positions = positions;
+  a.pos64 = position_bytes == 8;
+  a.pos_stride = position_stride;
+  a.offset = offset;
+  a.magnitude = magnitude;
+  a.sine = inverse ? -magnitude : magnitude;
+  for (int j = 0; j < rot / 2; ++j) a.turns[j] = inv_freq[j] / 6.283185307179586476925286766559;
+  int sms = 0;
+  BPT_TRY(check_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((a.tokens + a.tile - 1) / a.tile, (a.units + a.chunk - 1) / a.chunk);
+  {
+    LaunchScope ls("rotary", st);
+    if (es == 2 && w == 8)
+      launch_rotary<__nv_bfloat16, 8>(a, interleaved, grid, st);
+    else if (es == 2)
+      launch_rotary<__nv_bfloat16, 1>(a, interleaved, grid, st);
+    else if (w == 4)
+      launch_rotary<float, 4>(a, interleaved, grid, st);
+    else
+      launch_rotary<float, 1>(a, interleaved, grid, st);
+  }
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+size_t bpt_kv4_cache_bytes(int b, int kv_heads, int capacity, int dh) {
+  if (check_kv4(b, 0, kv_heads, capacity, dh) != BPT_OK) return 0;
+  return kv4_bytes(b, kv_heads, capacity, dh);
+}
+
+int bpt_kv4_store(void* cache, int b, int kv_heads, int capacity, int dh, const void* k, long long bs_k,
+                  long long ld_k, const void* v, long long bs_v, long long ld_v, int n, const int* start,
+                  const int* counts, void* stream) {
+  BPT_TRY(check_kv4(b, n, kv_heads, capacity, dh));
+  if (b == 0 || n == 0) return BPT_OK;
+  if (!cache || !k || !v || !start) return BPT_ERR_NULL;
+  const size_t width = (size_t)kv_heads * dh * 2;
+  const TokenRows rk{k, b, n, bs_k * 2, ld_k * 2, width}, rv{v, b, n, bs_v * 2, ld_v * 2, width};
+  if (!strides_ok(rk) || !strides_ok(rv)) return BPT_ERR_SHAPE;
+  if (!aligned16(cache) || !aligned(rk, 16) || !aligned(rv, 16)) return BPT_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(start) | reinterpret_cast<uintptr_t>(counts)) & 3u) return BPT_ERR_ALIGN;
+  const Range rc = rng(cache, kv4_bytes(b, kv_heads, capacity, dh));
+  if (overlap(rc, rk.range()) || overlap(rc, rv.range()) || overlap(rc, rng(start, (size_t)b * 4)) ||
+      (counts && overlap(rc, rng(counts, (size_t)b * 4))))
+    return BPT_ERR_ALIAS;
+  int sms = 0;
+  BPT_TRY(check_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Kv4StoreArgs a{reinterpret_cast<uint8_t*>(cache), {b, kv_heads, capacity}};
+  a.x[0] = reinterpret_cast<const __nv_bfloat16*>(k);
+  a.x[1] = reinterpret_cast<const __nv_bfloat16*>(v);
+  a.bs[0] = bs_k;
+  a.bs[1] = bs_v;
+  a.ld[0] = ld_k;
+  a.ld[1] = ld_v;
+  a.n = n;
+  a.start = start;
+  a.counts = counts;
+  BPT_TRY(stream_status_word(st, &a.status));
+  const long long units = (long long)n * kv_heads * (dh / 8);
+  const dim3 grid((unsigned)((units + KV4_THREADS - 1) / KV4_THREADS), grid_y(b));
+  {
+    LaunchScope ls("kv4_store", st);
+    if (dh == 128)
+      kv4_store_kernel<128><<<grid, KV4_THREADS, 0, st>>>(a);
+    else
+      kv4_store_kernel<64><<<grid, KV4_THREADS, 0, st>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, const int* start, const int* lens,
+                 int n, void* k, void* v, void* stream) {
+  BPT_TRY(check_kv4(b, n, kv_heads, capacity, dh));
+  if (b == 0 || n == 0) return BPT_OK;
+  if (!cache || !k || !v || !lens) return BPT_ERR_NULL;
+  if (!aligned16(cache) || !aligned16(k) || !aligned16(v)) return BPT_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(start) | reinterpret_cast<uintptr_t>(lens)) & 3u) return BPT_ERR_ALIGN;
+  const size_t act = (size_t)b * n * kv_heads * dh * 2;
+  const Range outs[2] = {rng(k, act), rng(v, act)};
+  const Range in[3] = {rng(cache, kv4_bytes(b, kv_heads, capacity, dh)), rng(lens, (size_t)b * 4),
+                       rng(start, start ? (size_t)b * 4 : 0)};
+  if (overlap(outs[0], outs[1])) return BPT_ERR_ALIAS;
+  for (const Range& o : outs)
+    for (const Range& r : in)
+      if (overlap(o, r)) return BPT_ERR_ALIAS;
+  int sms = 0;
+  BPT_TRY(check_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Kv4LoadArgs a{reinterpret_cast<const uint8_t*>(cache), {b, kv_heads, capacity}};
+  a.x[0] = reinterpret_cast<__nv_bfloat16*>(k);
+  a.x[1] = reinterpret_cast<__nv_bfloat16*>(v);
+  a.n = n;
+  a.start = start;
+  a.lens = lens;
+  BPT_TRY(stream_status_word(st, &a.status));
+  const long long units = (long long)n * kv_heads * (dh / 8);
+  const dim3 grid((unsigned)((units + KV4_THREADS - 1) / KV4_THREADS), grid_y(b));
+  {
+    LaunchScope ls("kv4_load", st);
+    if (dh == 128)
+      kv4_load_kernel<128><<<grid, KV4_THREADS, 0, st>>>(a);
+    else
+      kv4_load_kernel<64><<<grid, KV4_THREADS, 0, st>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+size_t bpt_kv4_attention_workspace_bytes(int b, int n, int heads, int kv_heads, int capacity, int dh,
+                                         int with_weights) {
+  if (check_kv4_attention(b, n, heads, kv_heads, capacity, dh) != BPT_OK || b == 0 || n == 0) return 0;
+  return kv4_attn_layout(b, n, heads, capacity, with_weights != 0).total;
+}
+
+int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void* cache, const int* lens, int b,
+                      int n, int heads, int kv_heads, int capacity, int dh, int causal, void* o, float* lse2,
+                      float* weights, void* workspace, size_t ws_bytes, void* stream) {
+  BPT_TRY(check_kv4_attention(b, n, heads, kv_heads, capacity, dh));
+  if (b == 0 || n == 0) return BPT_OK;
+  if (!q || !cache || !lens || !o || !workspace) return BPT_ERR_NULL;
+  const TokenRows rq{q, b, n, bs_q * 2, ld_q * 2, (size_t)heads * dh * 2};
+  if (!strides_ok(rq)) return BPT_ERR_SHAPE;
+  if (!aligned16(cache) || !aligned(rq, 16) || !aligned16(o) || !aligned16(lse2) || !aligned16(weights))
+    return BPT_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(lens) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return BPT_ERR_ALIGN;
+  const Kv4AttnLayout L = kv4_attn_layout(b, n, heads, capacity, weights != nullptr);
+  if (ws_bytes < L.total) return BPT_ERR_NOMEM;
+  const size_t rows = (size_t)b * n * heads;
+  const Range in[3] = {rq.range(), rng(cache, kv4_bytes(b, kv_heads, capacity, dh)), rng(lens, (size_t)b * 4)};
+  const Range outs[4] = {rng(o, rows * dh * 2), rng(lse2, lse2 ? rows * 4 : 0),
+                         rng(weights, weights ? (size_t)b * kv_heads * capacity * 4 : 0), rng(workspace, L.total)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& r : in)
+      if (overlap(outs[i], r)) return BPT_ERR_ALIAS;
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(outs[i], outs[j])) return BPT_ERR_ALIAS;
+  }
+  int sms = 0;
+  BPT_TRY(check_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  Kv4AttnArgs a{};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.bs_q = bs_q;
+  a.ld_q = ld_q;
+  a.cache = reinterpret_cast<const uint8_t*>(cache);
+  a.d = {b, kv_heads, capacity};
+  a.lens = lens;
+  a.n = n;
+  a.heads = heads;
+  a.causal = causal != 0;
+  a.score_scale = (float)(1.4426950408889634 / std::sqrt((double)dh));
+  a.o = reinterpret_cast<__nv_bfloat16*>(o);
+  a.lse2 = lse2 ? lse2 : reinterpret_cast<float*>(ws + L.lse);
+  a.scores = weights ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
+  BPT_TRY(stream_status_word(st, &a.status));
+  {
+    LaunchScope ls("kv4_attention", st);
+    const unsigned grid = (unsigned)std::min<size_t>(rows, 0x7fffffffu);
+    if (dh == 128)
+      kv4_attention_kernel<128><<<grid, KVA_THREADS, 0, st>>>(a);
+    else
+      kv4_attention_kernel<64><<<grid, KVA_THREADS, 0, st>>>(a);
+  }
+  if (weights) {
+    LaunchScope ls("kv4_weights", st);
+    const Kv4WeightsArgs w{a.scores, a.lse2, weights, a.d, lens, n, heads, a.causal};
+    const dim3 grid((unsigned)((capacity + KVA_THREADS - 1) / KVA_THREADS), grid_y((long long)b * kv_heads));
+    kv4_weights_kernel<<<grid, KVA_THREADS, 0, st>>>(w);
+  }
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+int bpt_kv4_evict(const void* cache, const float* weights, const int* lens, int b, int kv_heads, int capacity,
+                  int dh, int keep, int recent, void* cache_out, int capacity_out, float* weights_out, int* lens_out,
+                  int* kept, void* stream) {
+  BPT_TRY(check_kv4(b, 0, kv_heads, capacity, dh));
+  BPT_TRY(check_kv4(b, 0, kv_heads, capacity_out, dh));
+  if (keep <= 0 || keep > capacity_out || recent < 0 || recent > keep) return BPT_ERR_SHAPE;
+  if (b == 0) return BPT_OK;
+  if (!cache || !weights || !lens || !cache_out || !weights_out || !lens_out || !kept) return BPT_ERR_NULL;
+  const void* wide[4] = {cache, cache_out, weights, weights_out};
+  for (const void* p : wide)
+    if (!aligned16(p)) return BPT_ERR_ALIGN;
+  const void* ints[3] = {lens, lens_out, kept};
+  for (const void* p : ints)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return BPT_ERR_ALIGN;
+  const size_t rows = (size_t)b * kv_heads;
+  const Range in[3] = {rng(cache, kv4_bytes(b, kv_heads, capacity, dh)), rng(weights, rows * capacity * 4),
+                       rng(lens, (size_t)b * 4)};
+  const Range outs[4] = {rng(cache_out, kv4_bytes(b, kv_heads, capacity_out, dh)),
+                         rng(weights_out, rows * capacity_out * 4), rng(lens_out, (size_t)b * 4),
+                         rng(kept, rows * keep * 4)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& r : in)
+      if (overlap(outs[i], r)) return BPT_ERR_ALIAS;
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(outs[i], outs[j])) return BPT_ERR_ALIAS;
+  }
+  int sms = 0;
+  BPT_TRY(check_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int* status = nullptr;
+  BPT_TRY(stream_status_word(st, &status));
+  const Kv4Dims d{b, kv_heads, capacity}, d_out{b, kv_heads, capacity_out};
+  {
+    LaunchScope ls("kv4_select", st);
+    const Kv4SelectArgs a{weights, d, lens, keep, recent, kept, lens_out, status};
+    kv4_select_kernel<<<(unsigned)rows, EVICT_THREADS, 0, st>>>(a);
+  }
+  {
+    LaunchScope ls("kv4_move", st);
+    const Kv4MoveArgs a{reinterpret_cast<const uint8_t*>(cache), reinterpret_cast<uint8_t*>(cache_out), d, d_out,
+                        weights, weights_out, kept, lens_out, keep};
+    const int team = dh == 128 ? 8 : 4, per = KV4_THREADS / team;
+    const dim3 grid((unsigned)((capacity_out + per - 1) / per), grid_y((long long)rows));
+    if (dh == 128)
+      kv4_move_kernel<128><<<grid, KV4_THREADS, 0, st>>>(a);
+    else
+      kv4_move_kernel<64><<<grid, KV4_THREADS, 0, st>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -77,7 +77,8 @@ typedef enum bpt_status {
   BPT_ERR_CUDA = -7,        /* a CUDA runtime / driver call failed */
   BPT_ERR_TIMEOUT = -8,     /* a kernel gave up a bounded wait (device-side) */
   BPT_ERR_UNSUPPORTED = -9, /* the current device is not sm_100 */
-  BPT_ERR_DTYPE = -10       /* unknown dtype code */
+  BPT_ERR_DTYPE = -10,      /* unknown dtype code */
+  BPT_ERR_RANGE = -11       /* a length, start or count in device memory points outside the cache (device-side) */
 } bpt_status;
 
 typedef enum bpt_dtype {
@@ -438,6 +439,127 @@ int bpt_layer_backward_saved(const void* x, const void* Wqkv, const void* bqkv, 
                              const float* lse2_saved, const float* dy, int b, int s, int h, int heads, int ffn,
                              int causal, float* dx, float* dWqkv, float* dbqkv, float* dWo, float* dbo, float* dW1,
                              float* db1, float* dW2, float* db2, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions of queries and keys. The pages' layer has no positions and
+ * no counterpart to this section.
+ * ------------------------------------------------------------------------ */
+
+/* How a long context scales the angles (bpt_rotary_frequencies). */
+#define BPT_ROTARY_PLAIN 0  /* f_j = base^(-2j / rot) */
+#define BPT_ROTARY_LINEAR 1 /* f_j / factor: positions of the long context squeezed into the original one */
+#define BPT_ROTARY_BASE 2   /* base * factor^(rot / (rot - 2)): the slowest pair slows down by factor, the fastest stays */
+#define BPT_ROTARY_RAMP 3   /* pairs that turn fewer than low_turns times over the `original` tokens are divided by
+                               factor, those over high_turns times are left, those between are blended linearly; the
+                               magnitude is 0.1 ln(factor) + 1 */
+
+/* Radians per position of the rot / 2 pairs of a head, and the magnitude that
+ * goes with them, written to host memory (no CUDA call). factor >= 1; original,
+ * low_turns < high_turns are used by BPT_ROTARY_RAMP only. Errors:
+ * BPT_ERR_SHAPE (rot odd or outside 2 .. 128, rot == 2 for BPT_ROTARY_BASE, a
+ * scaling, base, factor, original or range of turns that is none), BPT_ERR_NULL. */
+int bpt_rotary_frequencies(int rot, double base, int scaling, double factor, int original, double low_turns,
+                           double high_turns, double* inv_freq, float* magnitude);
+
+/* Rotary positions of the queries and the keys, between bpt_qkv_projection and
+ * bpt_attention or bpt_kv4_store, in one launch: the first `rot` dimensions of
+ * each head of dh (64 or 128) are turned in pairs, the others copied,
+ *
+ *     y0 = m (x0 cos a - x1 sin a),  y1 = m (x1 cos a + x0 sin a),  a = pos inv_freq[j]
+ *
+ * with pair j being dimensions (j, j + rot / 2), or (2j, 2j + 1) if
+ * `interleaved`, and m = magnitude. `inverse` turns by -a: the transpose, which
+ * is the gradient (dq, dk of bpt_attention_backward in, the projection's out).
+ * dtype: bf16 or fp32 elements; the arithmetic is fp32, the angle fp64.
+ *
+ * q [b, s, heads * dh] and k [b, s, kv_heads * dh] have bs elements between
+ * sequences and ld between tokens, any non-negative strides (k may be NULL with
+ * kv_heads = 0); so have the outputs, whose rows must not overlap one another.
+ * An output may be its own input (same pointer and strides), or must not
+ * overlap any input; q and k may be columns of one buffer.
+ * positions: device memory, int32 or int64 (position_bytes 4 or 8), sequence
+ * beta's token t at beta * position_stride + t (0: every sequence the same); or
+ * NULL: token t is at offset + t. Angles keep fp32 accuracy for |position| up
+ * to 2^31. inv_freq: rot / 2 doubles in host memory, read during the call.
+ * Errors: BPT_ERR_DTYPE, BPT_ERR_SHAPE, BPT_ERR_NULL, BPT_ERR_ALIGN (pointers
+ * to their element's size), BPT_ERR_ALIAS; nothing launched then. */
+int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const void* k, long long bs_k,
+               long long ld_k, int b, int s, int heads, int kv_heads, int dh, int rot, int interleaved,
+               const double* inv_freq, float magnitude, const void* positions, int position_bytes,
+               long long position_stride, long long offset, int inverse, void* q_out, long long bs_qo,
+               long long ld_qo, void* k_out, long long bs_ko, long long ld_ko, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A key/value cache held in 4 bits, attention of new tokens over it, and
+ * eviction from it. The pages have no counterpart: they compute the attention
+ * of a whole sequence (bpt_attention); here its keys and values are kept for
+ * tokens that come later.
+ *
+ * The cache is one device buffer of bpt_kv4_cache_bytes bytes, 16-byte aligned,
+ * for b sequences, kv_heads key/value heads of dh (64 or 128) dimensions and
+ * `capacity` tokens (a positive multiple of 64) each; 4.5 bits an element. Per
+ * token, head and 64 dimensions: min, scale = bf16((max - min) / 15), code =
+ * rint((x - min) / scale) with the reciprocal of scale rounded to fp32; an
+ * element's value is min + scale * code. A group that holds an infinity or a
+ * NaN (or spans more than fp32's range) reads back as NaN. How many tokens a
+ * sequence holds is the caller's: int32 `lens` [b] in device memory. A length,
+ * start or count there that points outside the cache is cut to it and recorded
+ * as BPT_ERR_RANGE in the stream's status (bpt_stream_status).
+ *
+ * Errors of these calls: BPT_ERR_SHAPE, BPT_ERR_NULL, BPT_ERR_ALIGN (16 bytes;
+ * int32 arrays 4; strides of bf16 rows a multiple of 8 elements; the workspace
+ * 256), BPT_ERR_NOMEM (workspace too small), BPT_ERR_ALIAS (an output, the
+ * cache written or the workspace overlaps another argument); nothing launched
+ * then. All are asynchronous on `stream` and can be captured into a graph.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of a cache (0 for invalid arguments). */
+size_t bpt_kv4_cache_bytes(int b, int kv_heads, int capacity, int dh);
+
+/* Stores new tokens: token t of sequence beta (bf16 k and v rows of kv_heads *
+ * dh, bs elements between sequences and ld between tokens) goes to place
+ * start[beta] + t, for t < counts[beta] (counts NULL: for all n). Nothing else
+ * of the cache is written; a token whose place is outside the cache is dropped
+ * (BPT_ERR_RANGE in the stream's status). */
+int bpt_kv4_store(void* cache, int b, int kv_heads, int capacity, int dh, const void* k, long long bs_k,
+                  long long ld_k, const void* v, long long bs_v, long long ld_v, int n, const int* start,
+                  const int* counts, void* stream);
+
+/* Reads back, as bf16 [b, n, kv_heads * dh], the values that the cache holds at
+ * places start[beta] .. start[beta] + n - 1 (start NULL: from 0); places at or
+ * past lens[beta] read as zero. */
+int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, const int* start, const int* lens,
+                 int n, void* k, void* v, void* stream);
+
+/* Attention of the n newest tokens of each sequence over its cache, which holds
+ * them already (lens counts them): o = softmax(q K^T / sqrt(dh)) V per head,
+ * head i with key/value head i / (heads / kv_heads). With `causal` new token t
+ * sees the places below lens[beta] - n + 1 + t, otherwise all below lens[beta].
+ * A token that sees none gets zeros (and an lse2 of -infinity).
+ * q: bf16 rows of heads * dh, bs and ld as above; o: bf16 [b, n, heads * dh];
+ * lse2: fp32 [b, heads, n] as of bpt_attention_lse, or NULL. weights: fp32 [b,
+ * kv_heads, capacity], or NULL: every place's softmax weight, summed over the
+ * new tokens and the heads that share it, is ADDED to it (places at or past
+ * lens[beta] are left as they are). The scores and all sums are fp32; the
+ * softmax weights enter the product with V as bf16, times the scale of V. */
+size_t bpt_kv4_attention_workspace_bytes(int b, int n, int heads, int kv_heads, int capacity, int dh,
+                                         int with_weights);
+int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void* cache, const int* lens, int b,
+                      int n, int heads, int kv_heads, int capacity, int dh, int causal, void* o, float* lse2,
+                      float* weights, void* workspace, size_t ws_bytes, void* stream);
+
+/* Eviction by accumulated weight, into another cache: of sequence beta's len =
+ * lens[beta] tokens each key/value head keeps min(len, keep), namely the
+ * min(recent, keep, len) newest and the heaviest (by weights; equal ones: the
+ * lowest place; NaN heaviest) of the others, in the order of their places. Row
+ * j of the new cache (capacity_out >= keep tokens, the same b, kv_heads and dh)
+ * is the old row kept[j], bit for bit; rows past the kept ones are not written.
+ * kept: int32 [b, kv_heads, keep], -1 past the kept ones; weights_out: fp32 [b,
+ * kv_heads, capacity_out], the kept tokens' weights, then zeros; lens_out:
+ * int32 [b] = min(len, keep). 1 <= keep, 0 <= recent <= keep. */
+int bpt_kv4_evict(const void* cache, const float* weights, const int* lens, int b, int kv_heads, int capacity,
+                  int dh, int keep, int recent, void* cache_out, int capacity_out, float* weights_out, int* lens_out,
+                  int* kept, void* stream);
 
 /* ------------------------------------------------------------------------
  * Status and measurement.
