@@ -5,7 +5,28 @@
 //     lse2 = log2 sum_u 2^(c s_u),  c = log2 e,
 // with a running maximum and sum over one pass of the cache; the weights of a
 // cached token, summed over the queries that share its head, are added to
-// weights[u] by a second kernel from the scores that the first one leaves.
+// weights[u] by a further kernel from the scores that the first one leaves.
+//
+// Bound by HBM: 144 bytes a cached token and head (dh = 128) for 4 dh flops a
+// query, so the codes have to become matrix operands in as few instructions as
+// possible. The queries that share a head (heads / kv_heads times the new
+// tokens) are the 8 columns of m16n8k16 products, 16 cached tokens (K) or 16
+// dimensions (V) their rows:
+//     S^T[16 tokens, 8] = K[16, dh] Q^T,   O^T[dh, 8] += V^T[dh, 16] P^T.
+// A K nibble with one logical operation is the bf16 number 16 + code, a V
+// nibble 128 + code; scale and minimum enter after the product with K and
+// before the one with V:
+//     s   = sum over groups of scale (q . (16 + code) - 16 sum q) + min sum q
+//     o   = sum_u P' (128 + code) - 135.5 sum_u P' + sum_u p mid,
+// P' = bf16(p scale), mid = min + 7.5 scale: P' rounds what multiplies code -
+// 7.5, not code, and the sum of P' is one more product (with ones), so the
+// offset cancels to fp32 accuracy.
+//
+// The cached blocks of all sequences and heads, one after the other, are split
+// evenly over the warps of the device, whatever the lengths. A warp works on
+// its run alone: bulk copies into its own ring of stages, its own maximum, sum
+// and O^T; it leaves a partial result for each (sequence, head) that its run
+// touches, and kv4_join_kernel joins those.
 #pragma once
 
 #include "kv4_cache.cuh"
@@ -13,6 +34,23 @@
 namespace bpt {
 
 constexpr int KVA_THREADS = 256;
+constexpr int KVA_MAX_SMS = 148;      // the split does not grow past it (workspaces are sized without a device)
+constexpr float KVA_LAZY = 8.0f;      // the maximum is raised when a score passes it by this (log2)
+
+// Warps of an SM and stages of a warp: the rings take 216 KB in every case, and
+// the registers of that many warps hold what NT blocks of 8 columns need.
+template <int DH, int NT>
+struct KvaCfg {
+  static constexpr int WARPS = DH == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 16 : 12);
+  static constexpr int STAGES = DH == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 3 : 4);
+  static constexpr int RING = WARPS * STAGES * Kv4<DH>::BYTES;
+  static constexpr int SMEM = RING + WARPS * STAGES * 8 + 16 + 128;
+};
+
+inline int kva_warps(int dh, int nt) {
+  if (dh == 128) return nt == 1 ? KvaCfg<128, 1>::WARPS : KvaCfg<128, 2>::WARPS;
+  return nt == 1 ? KvaCfg<64, 1>::WARPS : KvaCfg<64, 2>::WARPS;
+}
 
 struct Kv4AttnArgs {
   const __nv_bfloat16* q;  // token (beta, t) at beta * bs + t * ld
@@ -21,10 +59,14 @@ struct Kv4AttnArgs {
   Kv4Dims d;
   const int* lens;         // [b], the new tokens among them
   int n, heads, causal;
+  int cols, cols_block, blocks_of_cols;  // queries that share a head; those of one pass over it; passes
+  int max_warps;
   float score_scale;       // log2(e) / sqrt(dh)
   __nv_bfloat16* o;        // [b, n, heads * dh]
   float* lse2;             // [b, heads, n]
-  float* scores;           // [b, kv_heads, group * n, capacity] in log2 units, or null
+  float* scores;           // [b, kv_heads, cols, capacity] in log2 units, or null
+  float* part_o;           // [slots][cols_block][dh]: sums of a run, not divided
+  float2* part_ml;         // [slots][cols_block]: maximum and sum
   int* status;
 };
 
@@ -33,92 +75,489 @@ __device__ __forceinline__ int kv4_seen(int len, int n, int t, int causal) {
   return causal ? max(len - n + 1 + t, 0) : len;
 }
 
-// One block a query: teams of dh/8 lanes take the cached tokens in turn, a lane
-// 8 dimensions of each, and the teams' sums are joined at the end.
-template <int DH>
-__global__ void __launch_bounds__(KVA_THREADS) kv4_attention_kernel(const Kv4AttnArgs a) {
-  constexpr int U = DH / 8, TEAMS = KVA_THREADS / U;
-  using L = Kv4<DH>;
-  __shared__ float s_o[TEAMS][DH], s_m[TEAMS], s_l[TEAMS];
-  const int group = a.heads / a.d.kv_heads;
-  const int u = threadIdx.x % U, team = threadIdx.x / U;
-  const long long queries = (long long)a.d.b * a.n * a.heads;
-  for (long long query = blockIdx.x; query < queries; query += gridDim.x) {
-    const int head = query % a.heads;
-    const long long tok = query / a.heads;
-    const int beta = tok / a.n, t = tok - (long long)beta * a.n;
-    const int kvh = head / group;
-    const int len = clamp_count(a.lens[beta], a.d.capacity, a.status);
-    const int seen = kv4_seen(len, a.n, t, a.causal);
-    const uint4 raw = *reinterpret_cast<const uint4*>(a.q + beta * a.bs_q + t * a.ld_q + head * DH + u * 8);
-    float q[8], o[8] = {}, m = -INFINITY, l = 0.f;
+// The even split. Segments are (sequence, head, block of columns) in that
+// order, T blocks of 64 tokens in all; warp w of W takes blocks T w / W up to T
+// (w + 1) / W, and its result for segment s goes to slot s + w (both grow along
+// the run, so no two share one).
+struct KvaSplit {
+  long long total;
+  int warps;
+  __device__ __forceinline__ long long first(int w) const { return total * w / warps; }
+  __device__ __forceinline__ int warp_of(long long block) const {
+    return (int)(((block + 1) * warps - 1) / total);
+  }
+};
+
+__device__ __forceinline__ int kva_blocks(const Kv4AttnArgs& a, int beta) {
+  return (min(max(a.lens[beta], 0), a.d.capacity) + KV4_BLOCK - 1) / KV4_BLOCK;
+}
+
+// Called by a whole warp: the split, and the blocks before sequence `beta`.
+__device__ __forceinline__ KvaSplit kva_split(const Kv4AttnArgs& a, int beta, long long& before) {
+  const long long per = (long long)a.d.kv_heads * a.blocks_of_cols;
+  long long total = 0, prior = 0;
+  for (int i = lane_id(); i < a.d.b; i += 32) {
+    const int nb = kva_blocks(a, i);
+    total += nb;
+    if (i < beta) prior += nb;
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&raw)[i]);
-      q[2 * i] = f.x;
-      q[2 * i + 1] = f.y;
-    }
-    const uint8_t* base = a.cache + ((long long)beta * a.d.kv_heads + kvh) * a.d.blocks() * L::BYTES;
-    float* scores = a.scores == nullptr
-                        ? nullptr
-                        : a.scores + (((long long)beta * a.d.kv_heads + kvh) * group * a.n +
-                                      (t * group + head - kvh * group)) * a.d.capacity;
-    const int rounds = (seen + TEAMS - 1) / TEAMS;
-    for (int k = 0; k < rounds; ++k) {
-      const int at = k * TEAMS + team;
-      const bool live = at < seen;
-      const int key = live ? at : 0, r = key % KV4_BLOCK;
-      const uint8_t* block = base + (long long)(key / KV4_BLOCK) * L::BYTES;
-      uint32_t wk = *reinterpret_cast<const uint32_t*>(block + r * L::ROW + kv4_k_place<DH>(u) * 4);
-      const uint32_t wv = *reinterpret_cast<const uint32_t*>(block + L::V_CODES + r * L::ROW + kv4_v_place<DH>(u, r) * 4);
-      const uint32_t pk = *reinterpret_cast<const uint32_t*>(block + L::K_PARAMS + r * L::PROW + u / 8 * 4);
-      const uint32_t pv = *reinterpret_cast<const uint32_t*>(block + L::V_PARAMS + r * L::PROW + u / 8 * 4);
-      wk = __funnelshift_r(wk, wk, 3);
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        dot = fmaf(q[i], fmaf((float)((wk >> (4 * i)) & 15u), __uint_as_float(pk << 16), __uint_as_float(pk & 0xffff0000u)), dot);
-#pragma unroll
-      for (int x = 1; x < U; x <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-      const float s = dot * a.score_scale;
-      if (!live) continue;
-      if (scores != nullptr && u == 0) scores[key] = s;
-      const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top;
-      const float keep = ex2_approx(m - ref), p = ex2_approx(s - ref);
-      m = top;
-      l = fmaf(l, keep, p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        o[i] = fmaf(o[i], keep, p * fmaf((float)((wv >> (4 * i)) & 15u), __uint_as_float(pv << 16), __uint_as_float(pv & 0xffff0000u)));
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s_o[team][u * 8 + i] = o[i];
-    if (u == 0) {
-      s_m[team] = m;
-      s_l[team] = l;
-    }
-    __syncthreads();
-    if (threadIdx.x < DH) {
-      float top = -INFINITY;
-      for (int x = 0; x < TEAMS; ++x) top = fmaxf(top, s_m[x]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float sum = 0.f, out = 0.f;
-      for (int x = 0; x < TEAMS; ++x) {
-        const float w = ex2_approx(s_m[x] - ref);
-        sum = fmaf(s_l[x], w, sum);
-        out = fmaf(s_o[x][threadIdx.x], w, out);
+  for (int o = 16; o; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    prior += __shfl_xor_sync(0xffffffffu, prior, o);
+  }
+  before = prior * per;
+  return KvaSplit{total * per, (int)max(1LL, min(total * per, (long long)a.max_warps))};
+}
+
+// A place in the run: block `blk` of row `row` (head and block of columns) of
+// sequence beta, which has nb blocks.
+struct KvaPlace {
+  int beta, row, blk, nb;
+  __device__ __forceinline__ void settle(const Kv4AttnArgs& a, int rows) {
+    while (blk >= nb && beta < a.d.b) {
+      blk = 0;
+      if (nb == 0 || ++row == rows) {
+        row = 0;
+        ++beta;
+        nb = beta < a.d.b ? kva_blocks(a, beta) : 0;
       }
-      const bool none = sum == 0.f;  // a row that sees no token is zero
-      a.o[query * DH + threadIdx.x] = __float2bfloat16_rn(none ? 0.f : out / sum);
-      if (threadIdx.x == 0) a.lse2[((long long)beta * a.heads + head) * a.n + t] = none ? -INFINITY : ref + log2f(sum);
     }
+  }
+};
+
+// The place of block t (whole warp).
+__device__ __forceinline__ KvaPlace kva_find(const Kv4AttnArgs& a, long long t, int rows) {
+  long long base = 0;
+  const int lane = lane_id();
+  for (int b0 = 0; b0 < a.d.b; b0 += 32) {
+    const int nb = b0 + lane < a.d.b ? kva_blocks(a, b0 + lane) : 0;
+    long long sum = (long long)nb * rows;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + sum > t);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      const int n = __shfl_sync(0xffffffffu, nb, src);
+      const long long r = t - (base + __shfl_sync(0xffffffffu, sum, src) - (long long)n * rows);
+      return KvaPlace{b0 + src, (int)(r / n), (int)(r % n), n};
+    }
+    base += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return KvaPlace{a.d.b, 0, 0, 0};
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of bf16 held two to a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int N>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+
+__device__ __forceinline__ float scale_of(uint32_t params) { return __uint_as_float(params << 16); }
+__device__ __forceinline__ float min_of(uint32_t params) { return __uint_as_float(params & 0xffff0000u); }
+
+// Lane (g, t) = (lane / 4, lane % 4). Row k of a 16-row product is the cached
+// token kva_token(k) of the 16: lane t of V's operand then reads rows t, 7 - t,
+// 8 + t and 15 - t, four neighbouring rows in every read of the warp, and the
+// two rows of K that 8 lanes read together lie in different halves of the banks.
+__device__ __forceinline__ int kva_token(int k) { return (k & 1) ? 7 - (k >> 1) : k >> 1; }
+
+// NT: blocks of 8 columns.
+template <int DH, int NT>
+__global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_kernel(const __grid_constant__ Kv4AttnArgs a) {
+  using L = Kv4<DH>;
+  using C = KvaCfg<DH, NT>;
+  constexpr int G = L::GROUPS, KW = DH / 32;  // groups; words of a K row that a lane takes
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem = (smem_addr(smem_raw) + 127u) & ~127u;
+  volatile int* flag = reinterpret_cast<volatile int*>(smem_raw + (smem - smem_addr(smem_raw)) + C::RING + C::WARPS * C::STAGES * 8);
+  const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem + warp * C::STAGES * L::BYTES;
+  const uint32_t bars = smem + C::RING + warp * C::STAGES * 8;
+  if (threadIdx.x == 0) *flag = 0;
+  if (lane == 0)
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(bars + i * 8, 1);
+  fence_mbar_init();
+  __syncthreads();
+  const Abort ab{flag, a.status};
+
+  long long unused;
+  const KvaSplit split = kva_split(a, 0, unused);
+  const int rows = a.d.kv_heads * a.blocks_of_cols;
+  if (blockIdx.x == 0 && warp == 0)
+    for (int i = lane; i < a.d.b; i += 32) clamp_count(a.lens[i], a.d.capacity, a.status);
+  const int w = warp * gridDim.x + blockIdx.x;  // neighbours of a run on different SMs
+  if (w >= split.warps || split.total == 0) return;
+  const long long t0 = split.first(w);
+  const int count = (int)(split.first(w + 1) - t0);
+  KvaPlace at = kva_find(a, t0, rows), next = at;
+
+  int issued = 0;
+  auto issue = [&]() {  // the next block of the run into its stage
+    if (issued >= count) return;
+    if (lane == 0) {
+      const uint32_t bar = bars + issued % C::STAGES * 8;
+      const uint8_t* src =
+          a.cache + (((long long)next.beta * a.d.kv_heads + next.row / a.blocks_of_cols) * a.d.blocks() + next.blk) * L::BYTES;
+      mbar_arrive_expect_tx(bar, L::BYTES);
+      bulk_load(ring + issued % C::STAGES * L::BYTES, src, L::BYTES, bar);
+    }
+    ++issued;
+    ++next.blk;
+    next.settle(a, rows);
+  };
+  for (int i = 0; i < C::STAGES; ++i) issue();
+
+  const int group = a.heads / a.d.kv_heads;
+  int done = 0;
+  while (done < count) {
+    // one segment's part of the run
+    const int len = min(max(a.lens[at.beta], 0), a.d.capacity);
+    const int kvh = at.row / a.blocks_of_cols, cb = at.row - kvh * a.blocks_of_cols;
+    const int col0 = cb * 8 * NT;
+    uint32_t qf[NT][KW][4];
+    float qs[NT][G][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int col = col0 + nt * 8 + g;
+      const bool real = col < a.cols;
+      const int tok = real ? col / group : 0, head = kvh * group + (real ? col - tok * group : 0);
+      const __nv_bfloat16* q = a.q + at.beta * a.bs_q + tok * a.ld_q + (long long)head * DH;
+      float sum[G] = {};
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const uint4 x = real ? *reinterpret_cast<const uint4*>(q + (i * 4 + t) * 8) : make_uint4(0, 0, 0, 0);
+        qf[nt][i][0] = __byte_perm(x.x, x.z, 0x5410);
+        qf[nt][i][1] = __byte_perm(x.x, x.z, 0x7632);
+        qf[nt][i][2] = __byte_perm(x.y, x.w, 0x5410);
+        qf[nt][i][3] = __byte_perm(x.y, x.w, 0x7632);
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[i / 2] += scale_of(y[e]) + min_of(y[e]);
+      }
+#pragma unroll
+      for (int gi = 0; gi < G; ++gi) {
+        sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 1);
+        sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qs[nt][gi][e] = __shfl_sync(0xffffffffu, sum[gi], (2 * t + e) * 4);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) lim[nt][e] = kv4_seen(len, a.n, (col0 + nt * 8 + 2 * t + e) / group, a.causal);
+    }
+    const int lim_all = kv4_seen(len, a.n, col0 / group, a.causal);  // seen by every column
+
+    float o[NT][G][4][4] = {}, ones[NT][G][4] = {};
+    float m[NT][2], l[NT][2] = {}, off[NT][G][2] = {};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
+
+    const int piece = min(at.nb - at.blk, count - done);
+    for (int k = 0; k < piece; ++k) {
+      const int stage = done % C::STAGES;
+      if (!warp_wait(bars + stage * 8, (done / C::STAGES) & 1, ab)) {
+        // the copies still in flight land before the warp leaves its ring
+        for (int i = done + 1; i < issued; ++i) {
+          const unsigned long long since = global_timer_ns();
+          while (!mbar_try_wait(bars + i % C::STAGES * 8, (i / C::STAGES) & 1) &&
+                 global_timer_ns() - since < kWaitTimeoutNs) {}
+        }
+        return;
+      }
+      const uint32_t blk = ring + stage * L::BYTES;
+      const int key0 = (at.blk + k) * KV4_BLOCK;
+      const bool whole = key0 + KV4_BLOCK <= lim_all;
+
+      float s[4][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const int ra = mt * 16 + kva_token(g), rb = ra + 8;
+        uint32_t ka[KW], kb[KW], pa[G], pb[G];
+        lds(blk + ra * L::ROW + t * (L::ROW / 4), ka);
+        lds(blk + rb * L::ROW + t * (L::ROW / 4), kb);
+        lds(blk + L::K_PARAMS + ra * L::PROW, pa);
+        lds(blk + L::K_PARAMS + rb * L::PROW, pb);
+        float acc[NT][G][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int gi = 0; gi < G; ++gi) {
+            acc[nt][gi][0] = acc[nt][gi][2] = -16.0f * qs[nt][gi][0];
+            acc[nt][gi][1] = acc[nt][gi][3] = -16.0f * qs[nt][gi][1];
+          }
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          uint32_t xa[4], xb[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            xa[e] = (__funnelshift_r(ka[i], ka[i], 4 * e) & 0x00780078u) | 0x41804180u;
+            xb[e] = (__funnelshift_r(kb[i], kb[i], 4 * e) & 0x00780078u) | 0x41804180u;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(acc[nt][i / 2], xa[0], xb[0], xa[1], xb[1], qf[nt][i][0], qf[nt][i][1]);
+            mma16816(acc[nt][i / 2], xa[2], xb[2], xa[3], xb[3], qf[nt][i][2], qf[nt][i][3]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t(&p)[G] = e < 2 ? pa : pb;
+            float x = 0.f;
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi)
+              x = fmaf(scale_of(p[gi]), acc[nt][gi][e], fmaf(min_of(p[gi]), qs[nt][gi][e & 1], x));
+            s[mt][nt][e] = x * a.score_scale;
+          }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + mt * 16 + kva_token(g) + (e >> 1) * 8 >= lim[nt][e & 1]) s[mt][nt][e] = -INFINITY;
+      }
+      if (a.scores != nullptr) {
+        float* to = a.scores + ((long long)at.beta * a.d.kv_heads + kvh) * a.cols * a.d.capacity + key0 + kva_token(g);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = col0 + nt * 8 + 2 * t + (e & 1);
+            if (col < a.cols)
+#pragma unroll
+              for (int mt = 0; mt < 4; ++mt) to[(long long)col * a.d.capacity + mt * 16 + (e >> 1) * 8] = s[mt][nt][e];
+          }
+      }
+
+      // the maximum: raised only where a score passes it by more than KVA_LAZY
+      bool grow = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+#pragma unroll
+          for (int mt = 1; mt < 4; ++mt) x = max3f(x, s[mt][nt][e], s[mt][nt][e + 2]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          top[nt][e] = x;
+          grow |= x > m[nt][e] + KVA_LAZY;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float now = fmaxf(m[nt][e], top[nt][e]);
+            const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - now);
+            m[nt][e] = now;
+            l[nt][e] *= f;
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) {
+              off[nt][gi][e] *= f;
+              ones[nt][gi][e] *= f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[nt][gi][i][e] *= f;
+                o[nt][gi][i][e + 2] *= f;
+              }
+            }
+          }
+      }
+      float ref[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ref[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const int ra = mt * 16 + kva_token(g);
+        uint32_t va[G], vb[G];
+        lds(blk + L::V_PARAMS + ra * L::PROW, va);
+        lds(blk + L::V_PARAMS + (ra + 8) * L::PROW, vb);
+        uint32_t bf[NT][G][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+          bool live[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2_approx(s[mt][nt][e] - ref[nt][e & 1]);
+            l[nt][e & 1] += p[e];
+            live[e] = whole || key0 + ra + (e >> 1) * 8 < lim[nt][e & 1];
+          }
+#pragma unroll
+          for (int gi = 0; gi < G; ++gi) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t pr = e < 2 ? va[gi] : vb[gi];
+              // a token that is not seen may have any parameters, NaN among them
+              x[e] = live[e] ? p[e] * scale_of(pr) : 0.f;
+              const float mid = fmaf(7.5f, scale_of(pr), min_of(pr));
+              if (live[e]) off[nt][gi][e & 1] = fmaf(p[e], mid, off[nt][gi][e & 1]);
+            }
+            bf[nt][gi][0] = transpose8(pack_bf16x2(x[0], x[1]));
+            bf[nt][gi][1] = transpose8(pack_bf16x2(x[2], x[3]));
+            mma16816(ones[nt][gi], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, bf[nt][gi][0], bf[nt][gi][1]);
+          }
+        }
+        uint32_t v[4][G];  // this lane's words of four tokens
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = mt * 16 + (j >> 1) * 8 + ((j & 1) ? 7 - t : t);
+          lds(blk + L::V_CODES + r * L::ROW + kv4_v_place<DH>(g, r) * 4, v[j]);
+        }
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi) {
+          const uint32_t lo0 = __byte_perm(v[0][gi], v[1][gi], 0x5410), hi0 = __byte_perm(v[0][gi], v[1][gi], 0x7632);
+          const uint32_t lo1 = __byte_perm(v[2][gi], v[3][gi], 0x5410), hi1 = __byte_perm(v[2][gi], v[3][gi], 0x7632);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = ((lo0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, a1 = ((hi0 >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+            const uint32_t a2 = ((lo1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, a3 = ((hi1 >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][gi][i], a0, a1, a2, a3, bf[nt][gi][0], bf[nt][gi][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      ++done;
+      issue();
+    }
+
+    // the run's sums for this segment
+    const long long slot = (long long)at.beta * rows + at.row + w;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[nt][e];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const int c = nt * 8 + 2 * t + e;
+        const bool real = col0 + c < a.cols;
+        const long long to = slot * a.cols_block + c;
+        if (real && g == 0) a.part_ml[to] = make_float2(m[nt][e], sum);
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi) {
+          float add = off[nt][gi][e];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
+          add = fmaf(-135.5f, ones[nt][gi][e], add);
+          if (real) {  // dimensions 8u .. 8u + 7 of word u = 8 gi + g
+            float4* dst = reinterpret_cast<float4*>(a.part_o + to * DH + (gi * 8 + g) * 8);
+            dst[0] = make_float4(o[nt][gi][0][e] + add, o[nt][gi][1][e] + add, o[nt][gi][2][e] + add, o[nt][gi][3][e] + add);
+            dst[1] = make_float4(o[nt][gi][0][e + 2] + add, o[nt][gi][1][e + 2] + add, o[nt][gi][2][e + 2] + add,
+                                 o[nt][gi][3][e + 2] + add);
+          }
+        }
+      }
+    at.blk += piece;
+    at.settle(a, rows);
+  }
+}
+
+constexpr int KVJ_WARPS = 4;
+
+// Joins the partial results of one (sequence, head, column): a warp takes every
+// KVJ_WARPS-th of them, a lane DH / 32 dimensions.
+template <int DH>
+__global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_constant__ Kv4AttnArgs a) {
+  constexpr int E = DH / 32;
+  __shared__ float s_m[KVJ_WARPS], s_l[KVJ_WARPS], s_o[KVJ_WARPS][DH];
+  const int warp = warp_id(), lane = lane_id();
+  const int rows = a.d.kv_heads * a.blocks_of_cols, group = a.heads / a.d.kv_heads;
+  const int kvh = blockIdx.x / a.cols, col = blockIdx.x - kvh * a.cols;
+  const int per = a.cols_block, cb = col / per, c = col - cb * per;
+  const int tok = col / group, head = kvh * group + col - tok * group;
+  for (int beta = blockIdx.y; beta < a.d.b; beta += gridDim.y) {
+    long long before;
+    const KvaSplit split = kva_split(a, beta, before);
+    const int nb = kva_blocks(a, beta), row = kvh * a.blocks_of_cols + cb;
+    float m = -INFINITY, l = 0.f, o[E] = {};
+    if (nb > 0) {
+      const long long first = before + (long long)row * nb;
+      const int w0 = split.warp_of(first), w1 = split.warp_of(first + nb - 1);
+      for (int w = w0 + warp; w <= w1; w += KVJ_WARPS) {
+        const long long at = ((long long)beta * rows + row + w) * a.cols_block + c;
+        const float2 ml = a.part_ml[at];
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = a.part_o[at * DH + lane * E + e];
+        const float now = fmaxf(m, ml.x), ref = now == -INFINITY ? 0.f : now;
+        const float f = ex2_approx(m - ref), k = ex2_approx(ml.x - ref);
+        m = now;
+        l = fmaf(l, f, ml.y * k);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f, x[e] * k);
+      }
+    }
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    __syncthreads();
+    float top = s_m[0];
+#pragma unroll
+    for (int i = 1; i < KVJ_WARPS; ++i) top = fmaxf(top, s_m[i]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < KVJ_WARPS; ++i) sum = fmaf(s_l[i], ex2_approx(s_m[i] - ref), sum);
+    const bool none = sum == 0.f;  // a row that sees no token is zero
+    if (threadIdx.x < DH) {
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < KVJ_WARPS; ++i) x = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - ref), x);
+      a.o[(((long long)beta * a.n + tok) * a.heads + head) * DH + threadIdx.x] = __float2bfloat16_rn(none ? 0.f : x / sum);
+    }
+    if (threadIdx.x == 0) a.lse2[((long long)beta * a.heads + head) * a.n + tok] = none ? -INFINITY : ref + log2f(sum);
     __syncthreads();
   }
 }
 
 struct Kv4WeightsArgs {
-  const float* scores;  // as Kv4AttnArgs
+  const float* scores;  // as in Kv4AttnArgs
   const float* lse2;    // [b, heads, n]
   float* weights;       // [b, kv_heads, capacity]
   Kv4Dims d;

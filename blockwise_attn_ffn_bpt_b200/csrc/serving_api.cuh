@@ -95,19 +95,45 @@ void launch_rotary(const RotaryArgs& a, bool interleaved, dim3 grid, cudaStream_
     rotary_kernel<T, W, false><<<grid, ROT_THREADS, 0, st>>>(a);
 }
 
+// Columns of one pass over a head's tokens, and the blocks of 8 of them: one
+// pass serves up to 16 queries that share a head, more take further passes
+// (whose blocks come from L2 where they fit).
+int kv4_col_blocks(int cols) { return cols <= 8 ? 1 : 2; }
+
 struct Kv4AttnLayout {
-  size_t lse = 0, scores = 0, total = 0;
+  size_t lse = 0, ml = 0, o = 0, scores = 0, total = 0;
+  int cols = 0, cols_block = 0, passes = 0, max_warps = 0;
 };
 
-Kv4AttnLayout kv4_attn_layout(int b, int n, int heads, int capacity, bool weights) {
+Kv4AttnLayout kv4_attn_layout(int b, int n, int heads, int kv_heads, int capacity, int dh, bool weights) {
   Kv4AttnLayout l;
+  l.cols = heads / kv_heads * n;
+  const int pass = 8 * kv4_col_blocks(l.cols);
+  l.cols_block = std::min(l.cols, pass);
+  l.passes = (l.cols + pass - 1) / pass;
+  const size_t segments = (size_t)b * kv_heads * l.passes;
+  const int warps = kva_warps(dh, pass / 8);
+  l.max_warps = (int)std::min<size_t>(segments * (capacity / KV4_BLOCK), (size_t)KVA_MAX_SMS * warps);
+  const size_t slots = segments + l.max_warps;
   size_t at = 0;
-  l.lse = at;
-  at += align_up((size_t)b * heads * n * 4, 256);
-  l.scores = at;
-  if (weights) at += align_up((size_t)b * heads * n * capacity * 4, 256);
+  auto take = [&](size_t& to, size_t bytes) {
+    to = at;
+    at += align_up(bytes, 256);
+  };
+  take(l.lse, (size_t)b * heads * n * 4);
+  take(l.ml, slots * l.cols_block * 8);
+  take(l.o, slots * l.cols_block * dh * 4);
+  if (weights) take(l.scores, (size_t)b * heads * n * capacity * 4);
   l.total = at;
   return l;
+}
+
+template <int DH, int NT>
+int launch_kv4_attention(const Kv4AttnArgs& a, int sms, cudaStream_t st) {
+  using C = KvaCfg<DH, NT>;
+  const unsigned grid = (unsigned)std::min({sms, KVA_MAX_SMS, (a.max_warps + C::WARPS - 1) / C::WARPS});
+  kv4_attention_kernel<DH, NT><<<grid, C::WARPS * 32, C::SMEM, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
 
 int check_kv4_attention(int b, int n, int heads, int kv_heads, int capacity, int dh) {
@@ -314,7 +340,7 @@ int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, c
 size_t bpt_kv4_attention_workspace_bytes(int b, int n, int heads, int kv_heads, int capacity, int dh,
                                          int with_weights) {
   if (check_kv4_attention(b, n, heads, kv_heads, capacity, dh) != BPT_OK || b == 0 || n == 0) return 0;
-  return kv4_attn_layout(b, n, heads, capacity, with_weights != 0).total;
+  return kv4_attn_layout(b, n, heads, kv_heads, capacity, dh, with_weights != 0).total;
 }
 
 int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void* cache, const int* lens, int b,
@@ -328,7 +354,7 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   if (!aligned16(cache) || !aligned(rq, 16) || !aligned16(o) || !aligned16(lse2) || !aligned16(weights))
     return BPT_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(lens) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return BPT_ERR_ALIGN;
-  const Kv4AttnLayout L = kv4_attn_layout(b, n, heads, capacity, weights != nullptr);
+  const Kv4AttnLayout L = kv4_attn_layout(b, n, heads, kv_heads, capacity, dh, weights != nullptr);
   if (ws_bytes < L.total) return BPT_ERR_NOMEM;
   const size_t rows = (size_t)b * n * heads;
   const Range in[3] = {rq.range(), rng(cache, kv4_bytes(b, kv_heads, capacity, dh)), rng(lens, (size_t)b * 4)};
@@ -358,14 +384,28 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
   a.lse2 = lse2 ? lse2 : reinterpret_cast<float*>(ws + L.lse);
   a.scores = weights ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
+  a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+  a.part_o = reinterpret_cast<float*>(ws + L.o);
+  a.cols = L.cols;
+  a.cols_block = L.cols_block;
+  a.blocks_of_cols = L.passes;
+  const int nt = kv4_col_blocks(L.cols);
+  a.max_warps = std::min(L.max_warps, std::min(sms, KVA_MAX_SMS) * kva_warps(dh, nt));
   BPT_TRY(stream_status_word(st, &a.status));
   {
     LaunchScope ls("kv4_attention", st);
-    const unsigned grid = (unsigned)std::min<size_t>(rows, 0x7fffffffu);
     if (dh == 128)
-      kv4_attention_kernel<128><<<grid, KVA_THREADS, 0, st>>>(a);
+      BPT_TRY(nt == 1 ? (launch_kv4_attention<128, 1>(a, sms, st)) : (launch_kv4_attention<128, 2>(a, sms, st)));
     else
-      kv4_attention_kernel<64><<<grid, KVA_THREADS, 0, st>>>(a);
+      BPT_TRY(nt == 1 ? (launch_kv4_attention<64, 1>(a, sms, st)) : (launch_kv4_attention<64, 2>(a, sms, st)));
+  }
+  {
+    LaunchScope ls("kv4_join", st);
+    const dim3 grid((unsigned)(kv_heads * L.cols), grid_y(b));
+    if (dh == 128)
+      kv4_join_kernel<128><<<grid, KVJ_WARPS * 32, 0, st>>>(a);
+    else
+      kv4_join_kernel<64><<<grid, KVJ_WARPS * 32, 0, st>>>(a);
   }
   if (weights) {
     LaunchScope ls("kv4_weights", st);
