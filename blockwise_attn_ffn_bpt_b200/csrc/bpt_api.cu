@@ -226,14 +226,7 @@ int check_device(int* sms) {
                                         AttnBwdCfg<64>::SMEM_BYTES) == cudaSuccess &&
                    cudaFuncSetAttribute(attention_bwd_tcgen05<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         AttnBwdCfg<128>::SMEM_BYTES) == cudaSuccess &&
-                   cudaFuncSetAttribute(kv4_attention_kernel<64, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (KvaCfg<64, 1>::SMEM)) == cudaSuccess &&
-                   cudaFuncSetAttribute(kv4_attention_kernel<64, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (KvaCfg<64, 2>::SMEM)) == cudaSuccess &&
-                   cudaFuncSetAttribute(kv4_attention_kernel<128, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (KvaCfg<128, 1>::SMEM)) == cudaSuccess &&
-                   cudaFuncSetAttribute(kv4_attention_kernel<128, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (KvaCfg<128, 2>::SMEM)) == cudaSuccess &&
+                   kva_set_attributes() &&
                    cudaFuncSetAttribute(layer_mega_tcgen05<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         mega_smem_bytes<64>()) == cudaSuccess &&
                    cudaFuncSetAttribute(layer_mega_tcgen05<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -29,6 +29,8 @@
 // touches, and kv4_join_kernel joins those.
 #pragma once
 
+#include <type_traits>
+
 #include "kv4_cache.cuh"
 
 namespace bpt {
@@ -156,13 +158,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// d = A B + c
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // The transpose of an 8 x 8 matrix of bf16 held two to a lane.
@@ -191,12 +194,18 @@ __device__ __forceinline__ float min_of(uint32_t params) { return __uint_as_floa
 // two rows of K that 8 lanes read together lie in different halves of the banks.
 __device__ __forceinline__ int kva_token(int k) { return (k & 1) ? 7 - (k >> 1) : k >> 1; }
 
-// NT: blocks of 8 columns.
-template <int DH, int NT>
+// NT blocks of 8 columns. With fewer queries than columns (NT = 1, F > 1) the 8
+// columns hold F copies of 8 / F queries, and copy f meets only the f-th of F
+// groups of 16 tokens (its queries are zero in the products of the others), so
+// that one accumulator ends up with the scores of 16 F tokens and the softmax
+// costs a lane F times less; the copies' sums are added at the end of the run.
+template <int DH, int NT, int F>
 __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_kernel(const __grid_constant__ Kv4AttnArgs a) {
+  static_assert(NT == 1 || F == 1, "copies of the queries fill one block of columns");
   using L = Kv4<DH>;
   using C = KvaCfg<DH, NT>;
   constexpr int G = L::GROUPS, KW = DH / 32;  // groups; words of a K row that a lane takes
+  constexpr int CW = 8 / F, J = 4 / F;        // columns of a copy; accumulators that 64 tokens need
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (smem_addr(smem_raw) + 127u) & ~127u;
   volatile int* flag = reinterpret_cast<volatile int*>(smem_raw + (smem - smem_addr(smem_raw)) + C::RING + C::WARPS * C::STAGES * 8);
@@ -238,18 +247,21 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   for (int i = 0; i < C::STAGES; ++i) issue();
 
   const int group = a.heads / a.d.kv_heads;
+  const int fold = 2 * t / CW;           // the copy that this lane's two columns of a result belong to
+  const int row_fold = F == 1 ? 0 : g / CW;  // the copy that this lane's column of an operand belongs to
+  const float lazy = KVA_LAZY / a.score_scale;
   int done = 0;
   while (done < count) {
     // one segment's part of the run
     const int len = min(max(a.lens[at.beta], 0), a.d.capacity);
     const int kvh = at.row / a.blocks_of_cols, cb = at.row - kvh * a.blocks_of_cols;
     const int col0 = cb * 8 * NT;
-    uint32_t qf[NT][KW][4];
-    float qs[NT][G][2];
+    uint32_t qf[NT][F][KW][4];
+    float qs[NT][G][2], init[NT][G][4];
     int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int col = col0 + nt * 8 + g;
+      const int col = col0 + nt * 8 + g % CW;
       const bool real = col < a.cols;
       const int tok = real ? col / group : 0, head = kvh * group + (real ? col - tok * group : 0);
       const __nv_bfloat16* q = a.q + at.beta * a.bs_q + tok * a.ld_q + (long long)head * DH;
@@ -257,98 +269,85 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         const uint4 x = real ? *reinterpret_cast<const uint4*>(q + (i * 4 + t) * 8) : make_uint4(0, 0, 0, 0);
-        qf[nt][i][0] = __byte_perm(x.x, x.z, 0x5410);
-        qf[nt][i][1] = __byte_perm(x.x, x.z, 0x7632);
-        qf[nt][i][2] = __byte_perm(x.y, x.w, 0x5410);
-        qf[nt][i][3] = __byte_perm(x.y, x.w, 0x7632);
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[i / 2] += scale_of(y[e]) + min_of(y[e]);
+        const uint32_t z[4] = {__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632)};
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[nt][f][i][e] = row_fold == f ? z[e] : 0u;
       }
 #pragma unroll
       for (int gi = 0; gi < G; ++gi) {
         sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 1);
         sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 2);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) qs[nt][gi][e] = __shfl_sync(0xffffffffu, sum[gi], (2 * t + e) * 4);
+        for (int e = 0; e < 2; ++e) {
+          qs[nt][gi][e] = __shfl_sync(0xffffffffu, sum[gi], (2 * t + e) * 4);
+          init[nt][gi][e] = init[nt][gi][e + 2] = -16.0f * qs[nt][gi][e];
+        }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) lim[nt][e] = kv4_seen(len, a.n, (col0 + nt * 8 + 2 * t + e) / group, a.causal);
+      for (int e = 0; e < 2; ++e) lim[nt][e] = kv4_seen(len, a.n, (col0 + nt * 8 + (2 * t + e) % CW) / group, a.causal);
     }
     const int lim_all = kv4_seen(len, a.n, col0 / group, a.causal);  // seen by every column
 
+    // m: the maximum's reference, in units of a score before score_scale; the
+    // sums of a lane are of its own tokens until the end of the run
     float o[NT][G][4][4] = {}, ones[NT][G][4] = {};
     float m[NT][2], l[NT][2] = {}, off[NT][G][2] = {};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
 
-    const int piece = min(at.nb - at.blk, count - done);
-    for (int k = 0; k < piece; ++k) {
-      const int stage = done % C::STAGES;
-      if (!warp_wait(bars + stage * 8, (done / C::STAGES) & 1, ab)) {
-        // the copies still in flight land before the warp leaves its ring
-        for (int i = done + 1; i < issued; ++i) {
-          const unsigned long long since = global_timer_ns();
-          while (!mbar_try_wait(bars + i % C::STAGES * 8, (i / C::STAGES) & 1) &&
-                 global_timer_ns() - since < kWaitTimeoutNs) {}
-        }
-        return;
-      }
-      const uint32_t blk = ring + stage * L::BYTES;
-      const int key0 = (at.blk + k) * KV4_BLOCK;
-      const bool whole = key0 + KV4_BLOCK <= lim_all;
-
-      float s[4][NT][4];
+    // One block of 64 tokens. WHOLE: every column sees all of them.
+    auto block = [&](auto whole_tag, uint32_t blk, int key0) {
+      constexpr bool WHOLE = decltype(whole_tag)::value;
+      float s[J][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        const int ra = mt * 16 + kva_token(g), rb = ra + 8;
-        uint32_t ka[KW], kb[KW], pa[G], pb[G];
-        lds(blk + ra * L::ROW + t * (L::ROW / 4), ka);
-        lds(blk + rb * L::ROW + t * (L::ROW / 4), kb);
-        lds(blk + L::K_PARAMS + ra * L::PROW, pa);
-        lds(blk + L::K_PARAMS + rb * L::PROW, pb);
+      for (int j = 0; j < J; ++j) {
         float acc[NT][G][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int f = 0; f < F; ++f) {
+          const int ra = (j * F + f) * 16 + kva_token(g);
+          uint32_t ka[KW], kb[KW];
+          lds(blk + ra * L::ROW + t * (L::ROW / 4), ka);
+          lds(blk + (ra + 8) * L::ROW + t * (L::ROW / 4), kb);
 #pragma unroll
-          for (int gi = 0; gi < G; ++gi) {
-            acc[nt][gi][0] = acc[nt][gi][2] = -16.0f * qs[nt][gi][0];
-            acc[nt][gi][1] = acc[nt][gi][3] = -16.0f * qs[nt][gi][1];
-          }
+          for (int i = 0; i < KW; ++i) {
+            uint32_t xa[4], xb[4];
 #pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          uint32_t xa[4], xb[4];
+            for (int e = 0; e < 4; ++e) {
+              xa[e] = (__funnelshift_r(ka[i], ka[i], 4 * e) & 0x00780078u) | 0x41804180u;
+              xb[e] = (__funnelshift_r(kb[i], kb[i], 4 * e) & 0x00780078u) | 0x41804180u;
+            }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            xa[e] = (__funnelshift_r(ka[i], ka[i], 4 * e) & 0x00780078u) | 0x41804180u;
-            xb[e] = (__funnelshift_r(kb[i], kb[i], 4 * e) & 0x00780078u) | 0x41804180u;
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816(acc[nt][i / 2], xa[0], xb[0], xa[1], xb[1], qf[nt][i][0], qf[nt][i][1]);
-            mma16816(acc[nt][i / 2], xa[2], xb[2], xa[3], xb[3], qf[nt][i][2], qf[nt][i][3]);
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t(&b)[4] = qf[nt][f][i];
+              float(&d)[4] = acc[nt][i / 2];
+              mma16816(d, xa[0], xb[0], xa[1], xb[1], b[0], b[1], f == 0 && i % 2 == 0 ? init[nt][i / 2] : d);
+              mma16816(d, xa[2], xb[2], xa[3], xb[3], b[2], b[3], d);
+            }
           }
         }
+        const int ra = (j * F + fold) * 16 + kva_token(g);  // the tokens of this lane's results: ra and ra + 8
+        uint32_t pa[G], pb[G];
+        lds(blk + L::K_PARAMS + ra * L::PROW, pa);
+        lds(blk + L::K_PARAMS + (ra + 8) * L::PROW, pb);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t(&p)[G] = e < 2 ? pa : pb;
-            float x = 0.f;
+            float x = scale_of(p[0]) * acc[nt][0][e];
 #pragma unroll
-            for (int gi = 0; gi < G; ++gi)
-              x = fmaf(scale_of(p[gi]), acc[nt][gi][e], fmaf(min_of(p[gi]), qs[nt][gi][e & 1], x));
-            s[mt][nt][e] = x * a.score_scale;
+            for (int gi = 1; gi < G; ++gi) x = fmaf(scale_of(p[gi]), acc[nt][gi][e], x);
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) x = fmaf(min_of(p[gi]), qs[nt][gi][e & 1], x);
+            if (!WHOLE && key0 + ra + (e >> 1) * 8 >= lim[nt][e & 1]) x = -INFINITY;
+            s[j][nt][e] = x;
           }
-      }
-      if (!whole) {
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key0 + mt * 16 + kva_token(g) + (e >> 1) * 8 >= lim[nt][e & 1]) s[mt][nt][e] = -INFINITY;
       }
       if (a.scores != nullptr) {
         float* to = a.scores + ((long long)at.beta * a.d.kv_heads + kvh) * a.cols * a.d.capacity + key0 + kva_token(g);
@@ -356,10 +355,11 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int col = col0 + nt * 8 + 2 * t + (e & 1);
+            const int col = col0 + nt * 8 + (2 * t + (e & 1)) % CW;
             if (col < a.cols)
 #pragma unroll
-              for (int mt = 0; mt < 4; ++mt) to[(long long)col * a.d.capacity + mt * 16 + (e >> 1) * 8] = s[mt][nt][e];
+              for (int j = 0; j < J; ++j)
+                to[(long long)col * a.d.capacity + (j * F + fold) * 16 + (e >> 1) * 8] = s[j][nt][e] * a.score_scale;
           }
       }
 
@@ -372,20 +372,20 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         for (int e = 0; e < 2; ++e) {
           float x = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
 #pragma unroll
-          for (int mt = 1; mt < 4; ++mt) x = max3f(x, s[mt][nt][e], s[mt][nt][e + 2]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          for (int j = 1; j < J; ++j) x = max3f(x, s[j][nt][e], s[j][nt][e + 2]);
           top[nt][e] = x;
-          grow |= x > m[nt][e] + KVA_LAZY;
+          grow |= x > m[nt][e] + lazy;
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float now = fmaxf(m[nt][e], top[nt][e]);
-            const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - now);
+            float now = fmaxf(m[nt][e], top[nt][e]);
+#pragma unroll
+            for (int x = CW / 2; x < 32; x <<= 1)  // all lanes that hold this column or a copy of it
+              now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
+            const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx((m[nt][e] - now) * a.score_scale);
             m[nt][e] = now;
             l[nt][e] *= f;
 #pragma unroll
@@ -400,15 +400,10 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             }
           }
       }
-      float ref[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) ref[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        const int ra = mt * 16 + kva_token(g);
+      for (int j = 0; j < J; ++j) {
+        const int ra = (j * F + fold) * 16 + kva_token(g);
         uint32_t va[G], vb[G];
         lds(blk + L::V_PARAMS + ra * L::PROW, va);
         lds(blk + L::V_PARAMS + (ra + 8) * L::PROW, vb);
@@ -416,12 +411,11 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float p[4];
-          bool live[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = ex2_approx(s[mt][nt][e] - ref[nt][e & 1]);
+            const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1] * a.score_scale;
+            p[e] = ex2_approx(fmaf(s[j][nt][e], a.score_scale, -ref));
             l[nt][e & 1] += p[e];
-            live[e] = whole || key0 + ra + (e >> 1) * 8 < lim[nt][e & 1];
           }
 #pragma unroll
           for (int gi = 0; gi < G; ++gi) {
@@ -429,70 +423,138 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t pr = e < 2 ? va[gi] : vb[gi];
-              // a token that is not seen may have any parameters, NaN among them
-              x[e] = live[e] ? p[e] * scale_of(pr) : 0.f;
               const float mid = fmaf(7.5f, scale_of(pr), min_of(pr));
-              if (live[e]) off[nt][gi][e & 1] = fmaf(p[e], mid, off[nt][gi][e & 1]);
+              x[e] = p[e] * scale_of(pr);
+              // a token that is not seen may have any parameters, NaN among them
+              const bool live = WHOLE || key0 + ra + (e >> 1) * 8 < lim[nt][e & 1];
+              if (!live) x[e] = 0.f;
+              if (live) off[nt][gi][e & 1] = fmaf(p[e], mid, off[nt][gi][e & 1]);
             }
             bf[nt][gi][0] = transpose8(pack_bf16x2(x[0], x[1]));
             bf[nt][gi][1] = transpose8(pack_bf16x2(x[2], x[3]));
-            mma16816(ones[nt][gi], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, bf[nt][gi][0], bf[nt][gi][1]);
+            mma16816(ones[nt][gi], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, bf[nt][gi][0], bf[nt][gi][1],
+                     ones[nt][gi]);
           }
         }
-        uint32_t v[4][G];  // this lane's words of four tokens
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = mt * 16 + (j >> 1) * 8 + ((j & 1) ? 7 - t : t);
-          lds(blk + L::V_CODES + r * L::ROW + kv4_v_place<DH>(g, r) * 4, v[j]);
-        }
+        for (int f = 0; f < F; ++f) {
+          uint32_t v[4][G];  // this lane's words of four tokens
 #pragma unroll
-        for (int gi = 0; gi < G; ++gi) {
-          const uint32_t lo0 = __byte_perm(v[0][gi], v[1][gi], 0x5410), hi0 = __byte_perm(v[0][gi], v[1][gi], 0x7632);
-          const uint32_t lo1 = __byte_perm(v[2][gi], v[3][gi], 0x5410), hi1 = __byte_perm(v[2][gi], v[3][gi], 0x7632);
+          for (int x = 0; x < 4; ++x) {
+            const int r = (j * F + f) * 16 + (x >> 1) * 8 + ((x & 1) ? 7 - t : t);
+            lds(blk + L::V_CODES + r * L::ROW + kv4_v_place<DH>(g, r) * 4, v[x]);
+          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a0 = ((lo0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, a1 = ((hi0 >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-            const uint32_t a2 = ((lo1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, a3 = ((hi1 >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+          for (int gi = 0; gi < G; ++gi) {
+            const uint32_t lo0 = __byte_perm(v[0][gi], v[1][gi], 0x5410), hi0 = __byte_perm(v[0][gi], v[1][gi], 0x7632);
+            const uint32_t lo1 = __byte_perm(v[2][gi], v[3][gi], 0x5410), hi1 = __byte_perm(v[2][gi], v[3][gi], 0x7632);
+            uint32_t b[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][gi][i], a0, a1, a2, a3, bf[nt][gi][0], bf[nt][gi][1]);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) b[nt][x] = F == 1 || row_fold == f ? bf[nt][gi][x] : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a0 = ((lo0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, a1 = ((hi0 >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+              const uint32_t a2 = ((lo1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, a3 = ((hi1 >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][gi][i], a0, a1, a2, a3, b[nt][0], b[nt][1], o[nt][gi][i]);
+            }
           }
         }
       }
+    };
+
+    const int piece = min(at.nb - at.blk, count - done);
+    for (int k = 0; k < piece; ++k) {
+      const int stage = done % C::STAGES;
+      if (!warp_wait(bars + stage * 8, (done / C::STAGES) & 1, ab)) {
+        // the copies still in flight land before the warp leaves its ring
+        for (int i = done + 1; i < issued; ++i) {
+          const unsigned long long since = global_timer_ns();
+          while (!mbar_try_wait(bars + i % C::STAGES * 8, (i / C::STAGES) & 1) &&
+                 global_timer_ns() - since < kWaitTimeoutNs) {}
+        }
+        return;
+      }
+      const int key0 = (at.blk + k) * KV4_BLOCK;
+      if (key0 + KV4_BLOCK <= lim_all)
+        block(std::true_type{}, ring + stage * L::BYTES, key0);
+      else
+        block(std::false_type{}, ring + stage * L::BYTES, key0);
       __syncwarp();  // every lane has read the stage
       ++done;
       issue();
     }
 
-    // the run's sums for this segment
+    // the run's sums for this segment: over the lanes of a column and its copies
     const long long slot = (long long)at.beta * rows + at.row + w;
+    auto over_lanes = [](float x) {
+#pragma unroll
+      for (int y = CW / 2; y < 32; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
+      return x;
+    };
+    auto over_copies = [](float x) {
+#pragma unroll
+      for (int y = CW / 2; y < 4; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
+      return x;
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float sum = l[nt][e];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const float sum = over_lanes(l[nt][e]);
         const int c = nt * 8 + 2 * t + e;
-        const bool real = col0 + c < a.cols;
+        const bool real = 2 * t < CW && col0 + c < a.cols;
         const long long to = slot * a.cols_block + c;
-        if (real && g == 0) a.part_ml[to] = make_float2(m[nt][e], sum);
+        if (real && g == 0) a.part_ml[to] = make_float2(m[nt][e] * a.score_scale, sum);
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
-          float add = off[nt][gi][e];
+          const float add = fmaf(-135.5f, over_copies(ones[nt][gi][e]), over_lanes(off[nt][gi][e]));
+          float x[8];  // dimensions 8u .. 8u + 7 of word u = 8 gi + g
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
-          add = fmaf(-135.5f, ones[nt][gi][e], add);
-          if (real) {  // dimensions 8u .. 8u + 7 of word u = 8 gi + g
+          for (int i = 0; i < 4; ++i) {
+            x[i] = over_copies(o[nt][gi][i][e]) + add;
+            x[i + 4] = over_copies(o[nt][gi][i][e + 2]) + add;
+          }
+          if (real) {
             float4* dst = reinterpret_cast<float4*>(a.part_o + to * DH + (gi * 8 + g) * 8);
-            dst[0] = make_float4(o[nt][gi][0][e] + add, o[nt][gi][1][e] + add, o[nt][gi][2][e] + add, o[nt][gi][3][e] + add);
-            dst[1] = make_float4(o[nt][gi][0][e + 2] + add, o[nt][gi][1][e + 2] + add, o[nt][gi][2][e + 2] + add,
-                                 o[nt][gi][3][e + 2] + add);
+            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+            dst[1] = make_float4(x[4], x[5], x[6], x[7]);
           }
         }
       }
     at.blk += piece;
     at.settle(a, rows);
   }
+}
+
+// The kernel for `cols` queries that share a head: one block of columns up to 8
+// of them, with as many copies as fit; two blocks (16 a pass) above that.
+inline int kva_col_blocks(int cols) { return cols <= 8 ? 1 : 2; }
+
+typedef void (*KvaKernel)(const Kv4AttnArgs);
+template <int DH>
+KvaKernel kva_kernel(int cols) {
+  if (cols <= 2) return kv4_attention_kernel<DH, 1, 4>;
+  if (cols <= 4) return kv4_attention_kernel<DH, 1, 2>;
+  return cols <= 8 ? kv4_attention_kernel<DH, 1, 1> : kv4_attention_kernel<DH, 2, 1>;
+}
+
+template <int DH>
+int kva_smem(int cols) {
+  return cols <= 8 ? KvaCfg<DH, 1>::SMEM : KvaCfg<DH, 2>::SMEM;
+}
+
+inline bool kva_set_attributes() {
+  bool ok = true;
+  for (int cols : {2, 4, 8, 16}) {
+    ok = ok && cudaFuncSetAttribute(kva_kernel<64>(cols), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kva_smem<64>(cols)) == cudaSuccess;
+    ok = ok && cudaFuncSetAttribute(kva_kernel<128>(cols), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kva_smem<128>(cols)) == cudaSuccess;
+  }
+  return ok;
 }
 
 constexpr int KVJ_WARPS = 4;

@@ -95,11 +95,6 @@ void launch_rotary(const RotaryArgs& a, bool interleaved, dim3 grid, cudaStream_
     rotary_kernel<T, W, false><<<grid, ROT_THREADS, 0, st>>>(a);
 }
 
-// Columns of one pass over a head's tokens, and the blocks of 8 of them: one
-// pass serves up to 16 queries that share a head, more take further passes
-// (whose blocks come from L2 where they fit).
-int kv4_col_blocks(int cols) { return cols <= 8 ? 1 : 2; }
-
 struct Kv4AttnLayout {
   size_t lse = 0, ml = 0, o = 0, scores = 0, total = 0;
   int cols = 0, cols_block = 0, passes = 0, max_warps = 0;
@@ -108,7 +103,7 @@ struct Kv4AttnLayout {
 Kv4AttnLayout kv4_attn_layout(int b, int n, int heads, int kv_heads, int capacity, int dh, bool weights) {
   Kv4AttnLayout l;
   l.cols = heads / kv_heads * n;
-  const int pass = 8 * kv4_col_blocks(l.cols);
+  const int pass = 8 * kva_col_blocks(l.cols);  // more queries take further passes over the head's tokens
   l.cols_block = std::min(l.cols, pass);
   l.passes = (l.cols + pass - 1) / pass;
   const size_t segments = (size_t)b * kv_heads * l.passes;
@@ -126,14 +121,6 @@ Kv4AttnLayout kv4_attn_layout(int b, int n, int heads, int kv_heads, int capacit
   if (weights) take(l.scores, (size_t)b * heads * n * capacity * 4);
   l.total = at;
   return l;
-}
-
-template <int DH, int NT>
-int launch_kv4_attention(const Kv4AttnArgs& a, int sms, cudaStream_t st) {
-  using C = KvaCfg<DH, NT>;
-  const unsigned grid = (unsigned)std::min({sms, KVA_MAX_SMS, (a.max_warps + C::WARPS - 1) / C::WARPS});
-  kv4_attention_kernel<DH, NT><<<grid, C::WARPS * 32, C::SMEM, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
 
 int check_kv4_attention(int b, int n, int heads, int kv_heads, int capacity, int dh) {
@@ -389,15 +376,16 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   a.cols = L.cols;
   a.cols_block = L.cols_block;
   a.blocks_of_cols = L.passes;
-  const int nt = kv4_col_blocks(L.cols);
-  a.max_warps = std::min(L.max_warps, std::min(sms, KVA_MAX_SMS) * kva_warps(dh, nt));
+  const int warps = kva_warps(dh, kva_col_blocks(L.cols)), most = std::min(sms, KVA_MAX_SMS);
+  a.max_warps = std::min(L.max_warps, most * warps);
   BPT_TRY(stream_status_word(st, &a.status));
   {
     LaunchScope ls("kv4_attention", st);
+    const unsigned grid = (unsigned)std::min(most, (a.max_warps + warps - 1) / warps);
     if (dh == 128)
-      BPT_TRY(nt == 1 ? (launch_kv4_attention<128, 1>(a, sms, st)) : (launch_kv4_attention<128, 2>(a, sms, st)));
+      kva_kernel<128>(L.cols)<<<grid, warps * 32, kva_smem<128>(L.cols), st>>>(a);
     else
-      BPT_TRY(nt == 1 ? (launch_kv4_attention<64, 1>(a, sms, st)) : (launch_kv4_attention<64, 2>(a, sms, st)));
+      kva_kernel<64>(L.cols)<<<grid, warps * 32, kva_smem<64>(L.cols), st>>>(a);
   }
   {
     LaunchScope ls("kv4_join", st);
