@@ -63,6 +63,7 @@ struct Kv4AttnArgs {
   int n, heads, causal;
   int cols, cols_block, blocks_of_cols;  // queries that share a head; those of one pass over it; passes
   int max_warps;
+  uint32_t zero;
   float score_scale;       // log2(e) / sqrt(dh)
   __nv_bfloat16* o;        // [b, n, heads * dh]
   float* lse2;             // [b, heads, n]
@@ -168,6 +169,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
+// (x & mask) | MAGIC in one operation. The mask comes in a register: with two
+// constants the compiler makes two operations of it, and these are what the
+// kernel's arithmetic units spend most of their time on.
+template <uint32_t MAGIC>
+__device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t mask) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "n"(MAGIC));
+  return y;
+}
+
 // The transpose of an 8 x 8 matrix of bf16 held two to a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -250,6 +261,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   const int fold = 2 * t / CW;           // the copy that this lane's two columns of a result belong to
   const int row_fold = F == 1 ? 0 : g / CW;  // the copy that this lane's column of an operand belongs to
   const float lazy = KVA_LAZY / a.score_scale;
+  // zero is 0: values that the compiler does not know, so that they stay in registers
+  const uint32_t k_mask = 0x00780078u + a.zero, v_mask = 0x000f000fu + a.zero;
   int done = 0;
   while (done < count) {
     // one segment's part of the run
@@ -319,8 +332,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             uint32_t xa[4], xb[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              xa[e] = (__funnelshift_r(ka[i], ka[i], 4 * e) & 0x00780078u) | 0x41804180u;
-              xb[e] = (__funnelshift_r(kb[i], kb[i], 4 * e) & 0x00780078u) | 0x41804180u;
+              xa[e] = code_pair<0x41804180u>(__funnelshift_r(ka[i], ka[i], 4 * e), k_mask);
+              xb[e] = code_pair<0x41804180u>(__funnelshift_r(kb[i], kb[i], 4 * e), k_mask);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -455,8 +468,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
               for (int x = 0; x < 2; ++x) b[nt][x] = F == 1 || row_fold == f ? bf[nt][gi][x] : 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t a0 = ((lo0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, a1 = ((hi0 >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-              const uint32_t a2 = ((lo1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, a3 = ((hi1 >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+              const uint32_t a0 = code_pair<0x43004300u>(lo0 >> (4 * i), v_mask), a1 = code_pair<0x43004300u>(hi0 >> (4 * i), v_mask);
+              const uint32_t a2 = code_pair<0x43004300u>(lo1 >> (4 * i), v_mask), a3 = code_pair<0x43004300u>(hi1 >> (4 * i), v_mask);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][gi][i], a0, a1, a2, a3, b[nt][0], b[nt][1], o[nt][gi][i]);
             }
