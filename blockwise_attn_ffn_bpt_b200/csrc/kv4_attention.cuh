@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem + warp * C::STAGES * L::BYTES;
   const uint32_t bars = smem + C::RING + warp * C::STAGES * 8;
+  grid_dependents_start();
   if (threadIdx.x == 0) *flag = 0;
   if (lane == 0)
     for (int i = 0; i < C::STAGES; ++i) mbar_init(bars + i * 8, 1);
@@ -570,10 +571,13 @@ inline bool kva_set_attributes() {
   return ok;
 }
 
-constexpr int KVJ_WARPS = 4;
+constexpr int KVJ_WARPS = 8;
+constexpr int KVJ_UNROLL = 4;
 
 // Joins the partial results of one (sequence, head, column): a warp takes every
-// KVJ_WARPS-th of them, a lane DH / 32 dimensions.
+// KVJ_WARPS-th of them, KVJ_UNROLL in flight, a lane DH / 32 dimensions. It is
+// launched while the attention still runs and waits for it here, so that its
+// start costs nothing.
 template <int DH>
 __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_constant__ Kv4AttnArgs a) {
   constexpr int E = DH / 32;
@@ -583,26 +587,49 @@ __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_c
   const int kvh = blockIdx.x / a.cols, col = blockIdx.x - kvh * a.cols;
   const int per = a.cols_block, cb = col / per, c = col - cb * per;
   const int tok = col / group, head = kvh * group + col - tok * group;
+  grid_dependents_start();
+  bool waited = false;
   for (int beta = blockIdx.y; beta < a.d.b; beta += gridDim.y) {
     long long before;
     const KvaSplit split = kva_split(a, beta, before);
     const int nb = kva_blocks(a, beta), row = kvh * a.blocks_of_cols + cb;
-    float m = -INFINITY, l = 0.f, o[E] = {};
+    int w0 = 0, w1 = -1;
     if (nb > 0) {
       const long long first = before + (long long)row * nb;
-      const int w0 = split.warp_of(first), w1 = split.warp_of(first + nb - 1);
-      for (int w = w0 + warp; w <= w1; w += KVJ_WARPS) {
-        const long long at = ((long long)beta * rows + row + w) * a.cols_block + c;
-        const float2 ml = a.part_ml[at];
-        float x[E];
+      w0 = split.warp_of(first);
+      w1 = split.warp_of(first + nb - 1);
+    }
+    if (!waited) {
+      grid_dependency_wait();
+      waited = true;
+    }
+    const long long at0 = ((long long)beta * rows + row) * a.cols_block + c;
+    float m = -INFINITY, l = 0.f, o[E] = {};
+    for (int w = w0 + warp; w <= w1; w += KVJ_WARPS * KVJ_UNROLL) {
+      float2 ml[KVJ_UNROLL];
+      float x[KVJ_UNROLL][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = a.part_o[at * DH + lane * E + e];
-        const float now = fmaxf(m, ml.x), ref = now == -INFINITY ? 0.f : now;
-        const float f = ex2_approx(m - ref), k = ex2_approx(ml.x - ref);
-        m = now;
-        l = fmaf(l, f, ml.y * k);
+      for (int u = 0; u < KVJ_UNROLL; ++u) {
+        const int v = w + u * KVJ_WARPS;
+        const long long at = at0 + (long long)v * a.cols_block;
+        ml[u] = v <= w1 ? __ldcg(&a.part_ml[at]) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f, x[e] * k);
+        for (int e = 0; e < E; ++e) x[u][e] = v <= w1 ? __ldcg(&a.part_o[at * DH + e * 32 + lane]) : 0.f;
+      }
+      float now = m;
+#pragma unroll
+      for (int u = 0; u < KVJ_UNROLL; ++u) now = fmaxf(now, ml[u].x);
+      const float ref = now == -INFINITY ? 0.f : now, f = ex2_approx(m - ref);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+      for (int u = 0; u < KVJ_UNROLL; ++u) {
+        const float k = ex2_approx(ml[u].x - ref);
+        l = fmaf(ml[u].y, k, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(x[u][e], k, o[e]);
       }
     }
     if (lane == 0) {
@@ -610,7 +637,7 @@ __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_c
       s_l[warp] = l;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
     __syncthreads();
     float top = s_m[0];
 #pragma unroll
@@ -641,10 +668,11 @@ struct Kv4WeightsArgs {
 };
 
 // weights[u] += sum over the queries that share u's head of 2^(score - lse2).
-__global__ void __launch_bounds__(KVA_THREADS) kv4_weights_kernel(const Kv4WeightsArgs a) {
+__global__ void __launch_bounds__(KVA_THREADS) kv4_weights_kernel(const __grid_constant__ Kv4WeightsArgs a) {
   const int group = a.heads / a.d.kv_heads, cols = group * a.n;
   const int key = blockIdx.x * KVA_THREADS + threadIdx.x;
   const int rows = a.d.b * a.d.kv_heads;
+  grid_dependency_wait();
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     const int beta = row / a.d.kv_heads, kvh = row - beta * a.d.kv_heads;
     const int len = min(max(a.lens[beta], 0), a.d.capacity);

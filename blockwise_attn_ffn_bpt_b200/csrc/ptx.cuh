@@ -135,6 +135,14 @@ __device__ __forceinline__ bool counter_wait(const unsigned* cnt, unsigned targe
   }
 }
 
+// ---------------------------------------------------------------- dependent launches
+// A kernel launched with programmatic stream serialization starts once every
+// block of the one before it has called grid_dependents_start (or ended), and
+// must not touch what that one writes before grid_dependency_wait, which waits
+// for its end.
+__device__ __forceinline__ void grid_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

@@ -85,6 +85,22 @@ int check_kv4(int b, int n, int kv_heads, int capacity, int dh) {
   return BPT_OK;
 }
 
+// Launches a kernel that may start before the one ahead of it on the stream has
+// ended (it waits for that itself: grid_dependency_wait).
+template <typename Args>
+int launch_dependent(void (*kernel)(const Args), const Args& args, dim3 grid, unsigned threads, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
 unsigned grid_y(long long rows) { return (unsigned)std::min<long long>(rows, 65535); }
 
 template <typename T, int W>
@@ -214,6 +230,7 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
   a.dh = dh;
   a.rot = rot;
   a.units = (heads + kv_heads) * (dh / (2 * w));
+  while ((1 << a.head_shift) < dh / (2 * w)) ++a.head_shift;
   a.chunk = std::min(a.units, ROT_THREADS * ROT_UNROLL);
   a.tile = std::max(1, std::min(ROT_TABLE / (rot / 2), ROT_THREADS * ROT_UNROLL / a.units));
   a.positions = positions;
@@ -390,16 +407,13 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   {
     LaunchScope ls("kv4_join", st);
     const dim3 grid((unsigned)(kv_heads * L.cols), grid_y(b));
-    if (dh == 128)
-      kv4_join_kernel<128><<<grid, KVJ_WARPS * 32, 0, st>>>(a);
-    else
-      kv4_join_kernel<64><<<grid, KVJ_WARPS * 32, 0, st>>>(a);
+    BPT_TRY(launch_dependent(dh == 128 ? kv4_join_kernel<128> : kv4_join_kernel<64>, a, grid, KVJ_WARPS * 32, st));
   }
   if (weights) {
     LaunchScope ls("kv4_weights", st);
     const Kv4WeightsArgs w{a.scores, a.lse2, weights, a.d, lens, n, heads, a.causal};
     const dim3 grid((unsigned)((capacity + KVA_THREADS - 1) / KVA_THREADS), grid_y((long long)b * kv_heads));
-    kv4_weights_kernel<<<grid, KVA_THREADS, 0, st>>>(w);
+    BPT_TRY(launch_dependent(kv4_weights_kernel, w, grid, KVA_THREADS, st));
   }
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
