@@ -467,17 +467,18 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", 
 def _rows(t: torch.Tensor, name: str, width: int, dtypes, like: Optional[torch.Tensor] = None) -> tuple:
     """(pointer, elements between sequences, elements between tokens) of a CUDA
     tensor [b, s, width] whose rows are contiguous."""
+    shape, stride, dtype = t.shape, t.stride(), t.dtype
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != width:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [b, s, {width}]")
-    if like is not None and (t.shape[:2] != like.shape[:2] or t.device != like.device or t.dtype != like.dtype):
+    if dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {dtype}")
+    if len(shape) != 3 or shape[2] != width:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [b, s, {width}]")
+    if like is not None and (shape[:2] != like.shape[:2] or dtype != like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have the tokens, dtype and device of the first tensor")
-    if t.stride(2) != 1:
+    if stride[2] != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), stride[0], stride[1]
 
 
 class _On:
@@ -485,21 +486,21 @@ class _On:
     one) as torch's current ones, so that outputs and workspaces belong to the
     stream that uses them. Enters as the stream's handle."""
 
-    __slots__ = ("device", "stream", "ctx")
+    __slots__ = ("index", "stream", "ctx")
 
-    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        self.device, self.stream, self.ctx = device, stream, None
+    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        self.index, self.stream, self.ctx = index, stream, None
 
     def __enter__(self) -> int:
         if self.stream is not None:
             self.ctx = torch.cuda.stream(self.stream)
-        elif self.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.device)
+        elif self.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.index)
         if self.ctx is not None:
             self.ctx.__enter__()
-        return (self.stream if self.stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc) -> None:
         if self.ctx is not None:
@@ -541,7 +542,7 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], heads: int, kv_heads: int
         at, size = positions.data_ptr(), positions.element_size()
         step = positions.stride(0) if positions.dim() == 2 else 0
     dtype = BPT_DTYPE_F32 if q.dtype == torch.float32 else BPT_DTYPE_BF16
-    with _On(q.device, stream) as st:
+    with _On(q.get_device(), stream) as st:
         if q_out is None:
             q_out = torch.empty((b, s, heads * dh), dtype=q.dtype, device=q.device)
         pqo = _rows(q_out, "q_out", heads * dh, kinds, q)
@@ -614,7 +615,7 @@ def kv4_store(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, start: torch.Te
         raise ValueError(f"k must hold {cache.b} sequences on the cache's device")
     ps = cache._ints(start, "start")
     pc = None if counts is None else cache._ints(counts, "counts")
-    with _On(k.device, stream) as st:
+    with _On(k.get_device(), stream) as st:
         r = lib().bpt_kv4_store(*cache._args(), *pk, *pv, k.shape[1], ps, pc, st)
     _check(r, "bpt_kv4_store")
 
@@ -627,7 +628,7 @@ def kv4_load(cache: KV4Cache, lens: torch.Tensor, n: int, start: Optional[torch.
     pl = cache._ints(lens, "lens")
     ps = None if start is None else cache._ints(start, "start")
     dev = cache.data.device
-    with _On(dev, stream) as st:
+    with _On(dev.index, stream) as st:
         k, v = torch.empty((2, cache.b, n, cache.kv_heads * cache.dh), dtype=torch.bfloat16, device=dev)
         r = lib().bpt_kv4_load(*cache._args(), ps, pl, n, k.data_ptr(), v.data_ptr(), st)
     _check(r, "bpt_kv4_load")
@@ -650,7 +651,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, heads: i
     n, dev = q.shape[1], q.device
     data, b, kv_heads, capacity, dh = cache._args()
     nbytes = int(lib().bpt_kv4_attention_workspace_bytes(b, n, heads, kv_heads, capacity, dh, int(pw is not None)))
-    with _On(dev, stream) as st:
+    with _On(dev.index, stream) as st:
         o = torch.empty((b, n, heads * dh), dtype=torch.bfloat16, device=dev)
         lse2 = torch.empty((b, heads, n), dtype=torch.float32, device=dev) if return_lse else None
         ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
@@ -672,7 +673,7 @@ def kv4_evict(cache: KV4Cache, weights: torch.Tensor, lens: torch.Tensor, keep: 
         raise ValueError("out must have the sequences, heads and device of the cache")
     pw, pl = cache._floats(weights, "weights"), cache._ints(lens, "lens")
     data, b, kv_heads, capacity, dh = cache._args()
-    with _On(dev, stream) as st:
+    with _On(dev.index, stream) as st:
         kept = torch.empty((b, kv_heads, max(int(keep), 0)), dtype=torch.int32, device=dev)
         new_lens = torch.empty(b, dtype=torch.int32, device=dev)
         new_weights = torch.empty((b, kv_heads, out.capacity), dtype=torch.float32, device=dev)

@@ -231,8 +231,12 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
   a.rot = rot;
   a.units = (heads + kv_heads) * (dh / (2 * w));
   while ((1 << a.head_shift) < dh / (2 * w)) ++a.head_shift;
-  a.chunk = std::min(a.units, ROT_THREADS * ROT_UNROLL);
-  a.tile = std::max(1, std::min(ROT_TABLE / (rot / 2), ROT_THREADS * ROT_UNROLL / a.units));
+  // tokens of a block: up to what its table of angles holds, as long as that
+  // leaves a few rounds of blocks for every SM; a token of very many heads is
+  // shared by several blocks
+  a.chunk = std::min(a.units, ROT_CHUNK);
+  const long long blocks = (long long)KVA_MAX_SMS * ROT_BLOCKS * ROT_ROUNDS;
+  a.tile = (int)std::max<long long>(1, std::min<long long>(ROT_TABLE / (rot / 2), a.tokens / blocks));
   a.positions = positions;
   a.pos64 = position_bytes == 8;
   a.pos_stride = position_stride;
