@@ -9,6 +9,7 @@ functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -544,11 +545,11 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], heads: int, kv_heads: int
     dtype = BPT_DTYPE_F32 if q.dtype == torch.float32 else BPT_DTYPE_BF16
     with _On(q.get_device(), stream) as st:
         if q_out is None:
-            q_out = torch.empty((b, s, heads * dh), dtype=q.dtype, device=q.device)
+            q_out = q.new_empty((b, s, heads * dh))
         pqo = _rows(q_out, "q_out", heads * dh, kinds, q)
         if k is not None:
             if k_out is None:
-                k_out = torch.empty((b, s, kv_heads * dh), dtype=q.dtype, device=q.device)
+                k_out = q.new_empty((b, s, kv_heads * dh))
             pko = _rows(k_out, "k_out", kv_heads * dh, kinds, q)
         r = lib().bpt_rotary(dtype, *pq, *pk, b, s, heads, kv_heads, dh, 2 * inv_freq.numel(), int(bool(interleaved)),
                              inv_freq.data_ptr(), float(magnitude), at, size, step, int(offset), int(bool(inverse)),
@@ -629,10 +630,16 @@ def kv4_load(cache: KV4Cache, lens: torch.Tensor, n: int, start: Optional[torch.
     ps = None if start is None else cache._ints(start, "start")
     dev = cache.data.device
     with _On(dev.index, stream) as st:
-        k, v = torch.empty((2, cache.b, n, cache.kv_heads * cache.dh), dtype=torch.bfloat16, device=dev)
+        shape = (cache.b, n, cache.kv_heads * cache.dh)
+        k, v = cache.data.new_empty(shape, dtype=torch.bfloat16), cache.data.new_empty(shape, dtype=torch.bfloat16)
         r = lib().bpt_kv4_load(*cache._args(), ps, pl, n, k.data_ptr(), v.data_ptr(), st)
     _check(r, "bpt_kv4_load")
     return k, v
+
+
+@functools.lru_cache(maxsize=256)
+def _kv4_workspace_bytes(b: int, n: int, heads: int, kv_heads: int, capacity: int, dh: int, weights: bool) -> int:
+    return int(lib().bpt_kv4_attention_workspace_bytes(b, n, heads, kv_heads, capacity, dh, int(weights)))
 
 
 def kv4_attention(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, heads: int, causal: bool = True,
@@ -650,11 +657,11 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, heads: i
     pw = None if weights is None else cache._floats(weights, "weights")
     n, dev = q.shape[1], q.device
     data, b, kv_heads, capacity, dh = cache._args()
-    nbytes = int(lib().bpt_kv4_attention_workspace_bytes(b, n, heads, kv_heads, capacity, dh, int(pw is not None)))
+    nbytes = _kv4_workspace_bytes(b, n, heads, kv_heads, capacity, dh, pw is not None)
     with _On(dev.index, stream) as st:
-        o = torch.empty((b, n, heads * dh), dtype=torch.bfloat16, device=dev)
-        lse2 = torch.empty((b, heads, n), dtype=torch.float32, device=dev) if return_lse else None
-        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        o = q.new_empty((b, n, heads * dh))
+        lse2 = q.new_empty((b, heads, n), dtype=torch.float32) if return_lse else None
+        ws = cache.data.new_empty(max(nbytes, 1))
         r = lib().bpt_kv4_attention(*pq, data, pl, b, n, heads, kv_heads, capacity, dh, int(bool(causal)),
                                     o.data_ptr(), None if lse2 is None else lse2.data_ptr(), pw, ws.data_ptr(),
                                     ws.numel(), st)
@@ -674,9 +681,9 @@ def kv4_evict(cache: KV4Cache, weights: torch.Tensor, lens: torch.Tensor, keep: 
     pw, pl = cache._floats(weights, "weights"), cache._ints(lens, "lens")
     data, b, kv_heads, capacity, dh = cache._args()
     with _On(dev.index, stream) as st:
-        kept = torch.empty((b, kv_heads, max(int(keep), 0)), dtype=torch.int32, device=dev)
-        new_lens = torch.empty(b, dtype=torch.int32, device=dev)
-        new_weights = torch.empty((b, kv_heads, out.capacity), dtype=torch.float32, device=dev)
+        kept = lens.new_empty((b, kv_heads, max(int(keep), 0)))
+        new_lens = lens.new_empty(b)
+        new_weights = weights.new_empty((b, kv_heads, out.capacity))
         r = lib().bpt_kv4_evict(data, pw, pl, b, kv_heads, capacity, dh, int(keep), int(recent), out.data.data_ptr(),
                                 out.capacity, new_weights.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), st)
     _check(r, "bpt_kv4_evict")

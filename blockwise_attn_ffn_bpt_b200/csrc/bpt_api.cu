@@ -37,6 +37,7 @@
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
 #include "kv4_attention.cuh"
+#include "kv4_evict.cuh"
 #include "row_pieces.h"
 
 // The bf16 forward GEMMs run on SM pairs (gemm_pair.cuh) when this is 1, on
@@ -227,6 +228,8 @@ int check_device(int* sms) {
                    cudaFuncSetAttribute(attention_bwd_tcgen05<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         AttnBwdCfg<128>::SMEM_BYTES) == cudaSuccess &&
                    kva_set_attributes() &&
+                   cudaFuncSetAttribute(kv4_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        EVICT_CACHED * 4) == cudaSuccess &&
                    cudaFuncSetAttribute(layer_mega_tcgen05<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         mega_smem_bytes<64>()) == cudaSuccess &&
                    cudaFuncSetAttribute(layer_mega_tcgen05<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,

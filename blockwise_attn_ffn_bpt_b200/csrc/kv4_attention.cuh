@@ -667,24 +667,38 @@ struct Kv4WeightsArgs {
   int n, heads, causal;
 };
 
-// weights[u] += sum over the queries that share u's head of 2^(score - lse2).
+// weights[u] += sum over the queries that share u's head of 2^(score - lse2):
+// 4 cached tokens a thread. Bound by memory (the scores come from L2 where they
+// fit).
 __global__ void __launch_bounds__(KVA_THREADS) kv4_weights_kernel(const __grid_constant__ Kv4WeightsArgs a) {
   const int group = a.heads / a.d.kv_heads, cols = group * a.n;
-  const int key = blockIdx.x * KVA_THREADS + threadIdx.x;
+  const int key = (blockIdx.x * KVA_THREADS + threadIdx.x) * 4;
   const int rows = a.d.b * a.d.kv_heads;
   grid_dependency_wait();
+  if (key >= a.d.capacity) return;
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     const int beta = row / a.d.kv_heads, kvh = row - beta * a.d.kv_heads;
     const int len = min(max(a.lens[beta], 0), a.d.capacity);
     if (key >= len) continue;
     const float* s = a.scores + (long long)row * cols * a.d.capacity + key;
-    float sum = 0.f;
+    float4* to = reinterpret_cast<float4*>(a.weights + (long long)row * a.d.capacity + key);
+    const float4 old = *to;  // past the length nothing is added
+    float sum[4] = {};
+#pragma unroll 4
     for (int c = 0; c < cols; ++c) {
       const int t = c / group, head = kvh * group + c - t * group;
-      if (key < kv4_seen(len, a.n, t, a.causal))
-        sum += ex2_approx(s[(long long)c * a.d.capacity] - a.lse2[((long long)beta * a.heads + head) * a.n + t]);
+      const int seen = kv4_seen(len, a.n, t, a.causal);
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(s + (long long)c * a.d.capacity));
+      const float lse2 = a.lse2[((long long)beta * a.heads + head) * a.n + t];
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += key + e < seen ? ex2_approx(v[e] - lse2) : 0.f;
     }
-    a.weights[(long long)row * a.d.capacity + key] += sum;
+    const float w[4] = {old.x, old.y, old.z, old.w};
+    float now[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) now[e] = key + e < len ? w[e] + sum[e] : w[e];
+    *to = make_float4(now[0], now[1], now[2], now[3]);
   }
 }
 

@@ -81,52 +81,64 @@ struct Kv4StoreArgs {
   int* status;
 };
 
-// 16 bytes of x to the word of 8 codes, with the group's parameters.
-__device__ __forceinline__ uint32_t kv4_quantise(const uint4& raw, uint32_t& params) {
-  const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&raw);
-  // NaN-propagating extremes, over the 8 lanes that hold the group
-  __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(x[0], x[1]), __hmin2_nan(x[2], x[3]));
-  __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(x[0], x[1]), __hmax2_nan(x[2], x[3]));
+// 16 values of x (bf16, packed) to two words of codes, with the group's
+// parameters; 4 neighbouring lanes hold the 64 values of a group.
+__device__ __forceinline__ void kv4_quantise(const uint32_t (&raw)[8], uint32_t (&word)[2], uint32_t& params) {
+  const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(raw);
+  // NaN-propagating extremes, both as minimums: (min x, min -x)
+  __nv_bfloat162 lo2 = x[0], hi2 = x[0];
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
-    hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+  for (int i = 1; i < 8; ++i) {
+    lo2 = __hmin2_nan(lo2, x[i]);
+    hi2 = __hmax2_nan(hi2, x[i]);
   }
-  const __nv_bfloat16 lo16 = __hmin_nan(__low2bfloat16(lo2), __high2bfloat16(lo2));
+  __nv_bfloat162 ends = __halves2bfloat162(__hmin_nan(__low2bfloat16(lo2), __high2bfloat16(lo2)),
+                                           __hneg(__hmax_nan(__low2bfloat16(hi2), __high2bfloat16(hi2))));
+  ends = __hmin2_nan(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
+  ends = __hmin2_nan(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
+  const __nv_bfloat16 lo16 = __low2bfloat16(ends);
   const float lo = __bfloat162float(lo16);
-  const float range = __bfloat162float(__hmax_nan(__low2bfloat16(hi2), __high2bfloat16(hi2))) - lo;
-  if (!(range < __int_as_float(0x7f800000))) {  // not finite: the group reads back as NaN
-    params = 0x7fc00000u;
-    return 0;
-  }
+  const float range = -__high2float(ends) - lo;
+  const bool finite = range < __int_as_float(0x7f800000);  // else the group reads back as NaN
   const __nv_bfloat16 scale16 = __float2bfloat16_rn(__fdiv_rn(range, 15.0f));
   const float scale = __bfloat162float(scale16);
-  const bool live = scale >= 1.17549435e-38f;
+  const bool live = finite && scale >= 1.17549435e-38f;
   const float r = live ? __fdiv_rn(1.0f, scale) : 0.0f;
-  params = (live ? (uint32_t)__bfloat16_as_ushort(scale16) : 0u) | ((uint32_t)__bfloat16_as_ushort(lo16) << 16);
-  uint32_t word = 0;
+  params = !finite ? 0x7fc00000u
+                   : (live ? (uint32_t)__bfloat16_as_ushort(scale16) : 0u) | ((uint32_t)__bfloat16_as_ushort(lo16) << 16);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(x[i]);
-    // adding 1.5 * 2^23 rounds the exact product to a whole number, ties to
-    // even, and leaves it in the low bits; at most 15 (1 + 2^-8) before that
-    const float c0 = fmaf(f.x - lo, r, 12582912.0f), c1 = fmaf(f.y - lo, r, 12582912.0f);
-    word |= (__float_as_uint(c0) & 15u) << (8 * i);
-    word |= (__float_as_uint(c1) & 15u) << (8 * i + 4);
+  for (int w = 0; w < 2; ++w) {
+    // Adding 1.5 * 2^23 rounds the exact product to a whole number, ties to
+    // even, and leaves it (at most 15 (1 + 2^-8) before that) in the low bits
+    // of 0x4b400000; those constants add up to 0x4b400000 (16^8 - 1) / 15.
+    uint32_t sum = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      const float2 f = __bfloat1622float2(x[4 * w + i]);
+      sum = sum * 16u + __float_as_uint(fmaf(f.y - lo, r, 12582912.0f));
+      sum = sum * 16u + __float_as_uint(fmaf(f.x - lo, r, 12582912.0f));
+    }
+    word[w] = live ? sum - 0x4b400000u * 0x11111111u : 0u;
   }
-  return word;
 }
 
-// A thread takes 8 dimensions of K and of V of one token and head: 16 bytes
-// in, one word out each. Bound by HBM.
-template <int DH>
-__global__ void __launch_bounds__(KV4_THREADS) kv4_store_kernel(const Kv4StoreArgs a) {
-  constexpr int U = DH / 8;
+// 32 bytes that are read once.
+__device__ __forceinline__ void load_stream32(const void* p, uint32_t (&x)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+               : "l"(p));
+}
+
+// A thread takes 16 dimensions of K and of V of one token and head: 32 bytes
+// in, two words out of each. Bound by HBM.
+template <int DH, bool WIDE>
+__global__ void __launch_bounds__(KV4_THREADS) kv4_store_kernel(const __grid_constant__ Kv4StoreArgs a) {
+  constexpr int U = DH / 16;
   using L = Kv4<DH>;
   const unsigned i = blockIdx.x * (unsigned)KV4_THREADS + threadIdx.x;
   const int u = i % U;
   const unsigned rest = i / U;
-  const int t = rest / a.d.kv_heads, head = rest - (unsigned)t * a.d.kv_heads;
+  const int t = rest / (unsigned)a.d.kv_heads, head = rest - (unsigned)t * a.d.kv_heads;
   for (int beta = blockIdx.y; beta < a.d.b; beta += gridDim.y) {
     const int count = a.counts == nullptr ? a.n : clamp_count(a.counts[beta], a.n, a.status);
     const long long at = (long long)a.start[beta] + t;
@@ -135,22 +147,34 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_store_kernel(const Kv4StoreAr
       record_range(a.status);
       live = false;
     }
-    uint4 raw[2] = {};
+    uint32_t raw[2][8] = {};
     if (live) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-        raw[w] = __ldcs(reinterpret_cast<const uint4*>(a.x[w] + beta * a.bs[w] + t * a.ld[w] + head * DH + u * 8));
+      for (int w = 0; w < 2; ++w) {
+        const __nv_bfloat16* src = a.x[w] + beta * a.bs[w] + t * a.ld[w] + (head * DH + u * 16);
+        if (WIDE) {
+          load_stream32(src, raw[w]);
+        } else {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src)), y = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+          raw[w][0] = x.x, raw[w][1] = x.y, raw[w][2] = x.z, raw[w][3] = x.w;
+          raw[w][4] = y.x, raw[w][5] = y.y, raw[w][6] = y.z, raw[w][7] = y.w;
+        }
+      }
     }
-    uint32_t pk, pv;  // whole warps quantise: the extremes are shuffled between 8 lanes
-    const uint32_t wk = kv4_quantise(raw[0], pk), wv = kv4_quantise(raw[1], pv);
+    uint32_t pk, pv, wk[2], wv[2];  // whole warps quantise: the extremes are shuffled between 4 lanes
+    kv4_quantise(raw[0], wk, pk);
+    kv4_quantise(raw[1], wv, pv);
     if (!live) continue;
     const int r = at % KV4_BLOCK;
     uint8_t* block = a.cache + (((long long)beta * a.d.kv_heads + head) * a.d.blocks() + at / KV4_BLOCK) * L::BYTES;
-    *reinterpret_cast<uint32_t*>(block + r * L::ROW + kv4_k_place<DH>(u) * 4) = __funnelshift_l(wk, wk, 3);
-    *reinterpret_cast<uint32_t*>(block + L::V_CODES + r * L::ROW + kv4_v_place<DH>(u, r) * 4) = wv;
-    if (u % 8 == 0) {
-      *reinterpret_cast<uint32_t*>(block + L::K_PARAMS + r * L::PROW + u / 8 * 4) = pk;
-      *reinterpret_cast<uint32_t*>(block + L::V_PARAMS + r * L::PROW + u / 8 * 4) = pv;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      *reinterpret_cast<uint32_t*>(block + r * L::ROW + kv4_k_place<DH>(2 * u + w) * 4) = __funnelshift_l(wk[w], wk[w], 3);
+      *reinterpret_cast<uint32_t*>(block + L::V_CODES + r * L::ROW + kv4_v_place<DH>(2 * u + w, r) * 4) = wv[w];
+    }
+    if (u % 4 == 0) {
+      *reinterpret_cast<uint32_t*>(block + L::K_PARAMS + r * L::PROW + u / 4 * 4) = pk;
+      *reinterpret_cast<uint32_t*>(block + L::V_PARAMS + r * L::PROW + u / 4 * 4) = pv;
     }
   }
 }
@@ -171,7 +195,9 @@ __device__ __forceinline__ uint4 kv4_values(uint32_t word, uint32_t params) {
   uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float c0 = (float)((word >> (8 * i)) & 15u), c1 = (float)((word >> (8 * i + 4)) & 15u);
+    // 2^23 + c is exact in fp32, and so is c again
+    const float c0 = __uint_as_float(((word >> (8 * i)) & 15u) | 0x4b000000u) - 8388608.0f;
+    const float c1 = __uint_as_float(((word >> (8 * i + 4)) & 15u) | 0x4b000000u) - 8388608.0f;
     out[i] = pack_bf16x2(fmaf(c0, scale, lo), fmaf(c1, scale, lo));
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
@@ -179,7 +205,7 @@ __device__ __forceinline__ uint4 kv4_values(uint32_t word, uint32_t params) {
 
 // The store's mapping the other way round. Bound by HBM (its writes).
 template <int DH>
-__global__ void __launch_bounds__(KV4_THREADS) kv4_load_kernel(const Kv4LoadArgs a) {
+__global__ void __launch_bounds__(KV4_THREADS) kv4_load_kernel(const __grid_constant__ Kv4LoadArgs a) {
   constexpr int U = DH / 8;
   using L = Kv4<DH>;
   const unsigned i = blockIdx.x * (unsigned)KV4_THREADS + threadIdx.x;

@@ -15,6 +15,7 @@ namespace bpt {
 
 constexpr int EVICT_THREADS = 1024;
 constexpr int EVICT_BINS = 2048;
+constexpr int EVICT_CACHED = 49152;  // tokens whose keys fit in shared memory (192 KB)
 
 struct Kv4SelectArgs {
   const float* weights;  // [b, kv_heads, capacity]
@@ -34,12 +35,23 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return x ^ ((x >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const Kv4SelectArgs a) {
+// The keys of 4 weights. Past `old` they are 0, below every weight's.
+__device__ __forceinline__ uint4 weight_keys(const float4& w, int i, int old) {
+  return make_uint4(i < old ? weight_key(w.x) : 0u, i + 1 < old ? weight_key(w.y) : 0u,
+                    i + 2 < old ? weight_key(w.z) : 0u, i + 3 < old ? weight_key(w.w) : 0u);
+}
+
+// One block a (sequence, head). The keys of up to EVICT_CACHED tokens stay in
+// shared memory after the first pass; longer rows are read again, from L2.
+template <bool CACHED>
+__global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_constant__ Kv4SelectArgs a) {
+  extern __shared__ uint4 cached[];
   __shared__ int hist[EVICT_BINS];
   __shared__ int warp_sum[32], warp_tie[32];
   __shared__ int s_bin, s_need;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = a.d.b * a.d.kv_heads;
+  grid_dependents_start();
   for (int row = blockIdx.x; row < rows; row += gridDim.x) {
     const int beta = row / a.d.kv_heads;
     const int len = clamp_count(a.lens[beta], a.d.capacity, a.status);
@@ -48,24 +60,38 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const Kv4Sele
     const float* w = a.weights + (long long)row * a.d.capacity;
     int* kept = a.kept + (long long)row * a.keep;
     if (tid == 0 && row == beta * a.d.kv_heads) a.lens_out[beta] = left;
-    for (int i = tid; i < a.keep; i += EVICT_THREADS)
-      if (i >= need) kept[i] = i < left ? old + i - need : -1;
+    for (int i = need + tid; i < a.keep; i += EVICT_THREADS) kept[i] = i < left ? old + i - need : -1;
     if (need == old) {
       for (int i = tid; i < need; i += EVICT_THREADS) kept[i] = i;
       continue;
     }
     if (need == 0) continue;
+    const int quads = (old + 3) / 4;
+    auto keys_of = [&](int i, bool first) -> uint4 {
+      if (CACHED && !first) return cached[i];
+      const uint4 k = weight_keys(__ldg(reinterpret_cast<const float4*>(w) + i), 4 * i, old);
+      if (CACHED) cached[i] = k;
+      return k;
+    };
     // the need-th largest key, digit by digit
     uint32_t prefix = 0, mask = 0;
     int want = need;
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      const uint32_t digit = (1u << bits) - 1;
       __syncthreads();
       for (int i = tid; i < EVICT_BINS; i += EVICT_THREADS) hist[i] = 0;
       __syncthreads();
-      for (int i = tid; i < old; i += EVICT_THREADS) {
-        const uint32_t key = weight_key(w[i]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & ((1 << bits) - 1)], 1);
+      auto count = [&](uint32_t key) {
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1);
+      };
+#pragma unroll 4
+      for (int i = tid; i < quads; i += EVICT_THREADS) {
+        const uint4 k = keys_of(i, pass == 0);
+        count(k.x);
+        count(k.y);
+        count(k.z);
+        count(k.w);
       }
       __syncthreads();
       // from the top: thread i holds bins BINS - 1 - 2i and BINS - 2 - 2i
@@ -87,18 +113,19 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const Kv4Sele
       }
       __syncthreads();
       prefix |= (uint32_t)s_bin << shift;
-      mask |= (uint32_t)((1 << bits) - 1) << shift;
+      mask |= digit << shift;
       want = s_need;
     }
     // keys above `prefix` stay, and the first `want` of those equal to it;
-    // each warp takes a run of whole 32s and first counts what stays before it
-    const int run = ((old + 1023) / 1024) * 32;
-    const int lo = min(warp * run, old), hi = min(lo + run, old);
+    // each warp takes a run of whole 128s and first counts what stays before it
+    const int run = (quads + 1023) / 1024 * 32;
+    const int lo = min(warp * run, quads), hi = min(lo + run, quads);
     int more = 0, tie = 0;
+#pragma unroll 4
     for (int i = lo + lane; i < hi; i += 32) {
-      const uint32_t key = weight_key(w[i]);
-      more += key > prefix;
-      tie += key == prefix;
+      const uint4 k = keys_of(i, false);
+      more += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+      tie += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
     }
     more = __reduce_add_sync(0xffffffffu, more);
     tie = __reduce_add_sync(0xffffffffu, tie);
@@ -112,17 +139,31 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const Kv4Sele
       above += warp_sum[i];
       ties += warp_tie[i];
     }
-    const uint32_t below = (1u << lane) - 1;
     for (int i0 = lo; i0 < hi; i0 += 32) {
       const int i = i0 + lane;
-      const uint32_t key = i < hi ? weight_key(w[i]) : 0u;
-      const uint32_t m_above = __ballot_sync(0xffffffffu, i < hi && key > prefix);
-      const uint32_t m_tie = __ballot_sync(0xffffffffu, i < hi && key == prefix);
-      const int tie_at = ties + __popc(m_tie & below);
-      const bool stays = (m_above >> lane & 1) || ((m_tie >> lane & 1) && tie_at < want);
-      if (stays) kept[above + __popc(m_above & below) + min(tie_at, want)] = i;
-      above += __popc(m_above);
-      ties += __popc(m_tie);
+      const uint4 k4 = i < hi ? keys_of(i, false) : make_uint4(0, 0, 0, 0);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+      // counts above in the upper half, ties in the lower (at most 128 each)
+      int mine = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mine += k[e] > prefix ? 0x10000 : i < hi && k[e] == prefix ? 1 : 0;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const int all = __shfl_sync(0xffffffffu, upto, 31);
+      int at = above + ((upto - mine) >> 16), tied = ties + ((upto - mine) & 0xffff);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool is_above = k[e] > prefix, is_tie = i < hi && k[e] == prefix;
+        if (is_above || (is_tie && tied < want)) kept[at + min(tied, want)] = 4 * i + e;
+        at += is_above;
+        tied += is_tie;
+      }
+      above += all >> 16;
+      ties += all & 0xffff;
     }
     __syncthreads();
   }
@@ -139,44 +180,65 @@ struct Kv4MoveArgs {
   int keep;
 };
 
-// A team of lanes moves one row, 16 bytes of codes a lane, then its parameters
-// and weight. The halves of V's row change places where the two rows' places
-// differ in that bit (kv4_v_place). Bound by HBM.
+constexpr int MOVE_ROWS = 4;
+
+// A team of lanes moves MOVE_ROWS rows at a time, 16 bytes of codes of each a
+// lane, then their parameters and weights. The halves of V's row change places
+// where the two rows' places differ in that bit (kv4_v_place). Bound by HBM, and
+// by the latency of two reads in a row (a place, then its row): hence several
+// rows at once.
 template <int DH>
-__global__ void __launch_bounds__(KV4_THREADS) kv4_move_kernel(const Kv4MoveArgs a) {
+__global__ void __launch_bounds__(KV4_THREADS) kv4_move_kernel(const __grid_constant__ Kv4MoveArgs a) {
   using L = Kv4<DH>;
-  constexpr int C = L::ROW / 16, TEAM = 2 * C;  // 16-byte pieces of a row of codes; lanes: K's, then V's
+  constexpr int C = L::ROW / 16, TEAM = 2 * C, TEAMS = KV4_THREADS / TEAM;  // lanes: K's 16-byte pieces, then V's
   const int piece = threadIdx.x % TEAM;
-  const int j = blockIdx.x * (KV4_THREADS / TEAM) + threadIdx.x / TEAM;
+  const int j0 = blockIdx.x * (TEAMS * MOVE_ROWS) + threadIdx.x / TEAM;
   const int rows = a.d.b * a.d.kv_heads;
-  if (j >= a.d_out.capacity) return;
+  grid_dependency_wait();
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     const int left = a.lens_out[row / a.d.kv_heads];
-    if (j >= left) {
-      if (piece == 0) a.weights_out[(long long)row * a.d_out.capacity + j] = 0.f;
-      continue;
-    }
-    const int i = a.kept[(long long)row * a.keep + j];
-    const int ri = i % KV4_BLOCK, rj = j % KV4_BLOCK;
-    const uint8_t* from = a.src + ((long long)row * a.d.blocks() + i / KV4_BLOCK) * L::BYTES;
-    uint8_t* to = a.dst + ((long long)row * a.d_out.blocks() + j / KV4_BLOCK) * L::BYTES;
-    if (piece < C) {
-      *reinterpret_cast<uint4*>(to + rj * L::ROW + piece * 16) =
-          *reinterpret_cast<const uint4*>(from + ri * L::ROW + piece * 16);
-    } else {
-      const int c = piece - C;
-      const int swap = DH == 64 ? 0 : ((ri ^ rj) & 2);  // places differ by 4 pairs of words = 2 pieces
-      *reinterpret_cast<uint4*>(to + L::V_CODES + rj * L::ROW + (c ^ swap) * 16) =
-          *reinterpret_cast<const uint4*>(from + L::V_CODES + ri * L::ROW + c * 16);
-    }
-    if (piece < 2) {
-      const int at = piece == 0 ? L::K_PARAMS : L::V_PARAMS;
+    const uint8_t* src = a.src + (long long)row * a.d.blocks() * L::BYTES;
+    uint8_t* dst = a.dst + (long long)row * a.d_out.blocks() * L::BYTES;
+    int from[MOVE_ROWS];
 #pragma unroll
-      for (int g = 0; g < L::GROUPS; ++g)
-        *reinterpret_cast<uint32_t*>(to + at + rj * L::PROW + g * 4) =
-            *reinterpret_cast<const uint32_t*>(from + at + ri * L::PROW + g * 4);
-      if (piece == 0)
-        a.weights_out[(long long)row * a.d_out.capacity + j] = a.weights[(long long)row * a.d.capacity + i];
+    for (int k = 0; k < MOVE_ROWS; ++k) {
+      const int j = j0 + k * TEAMS;
+      from[k] = j < left ? a.kept[(long long)row * a.keep + j] : -1;
+    }
+    uint4 codes[MOVE_ROWS];
+    uint32_t params[MOVE_ROWS][L::GROUPS];
+    float weight[MOVE_ROWS];
+#pragma unroll
+    for (int k = 0; k < MOVE_ROWS; ++k) {
+      weight[k] = 0.f;
+      if (from[k] < 0) continue;
+      const int r = from[k] % KV4_BLOCK;
+      const uint8_t* block = src + (long long)(from[k] / KV4_BLOCK) * L::BYTES;
+      const int at = (piece < C ? 0 : L::V_CODES) + r * L::ROW + (piece < C ? piece : piece - C) * 16;
+      codes[k] = __ldg(reinterpret_cast<const uint4*>(block + at));
+      if (piece < 2) {
+#pragma unroll
+        for (int g = 0; g < L::GROUPS; ++g)
+          params[k][g] = __ldg(reinterpret_cast<const uint32_t*>(block + (piece == 0 ? L::K_PARAMS : L::V_PARAMS) + r * L::PROW) + g);
+      }
+      if (piece == 2) weight[k] = __ldg(a.weights + (long long)row * a.d.capacity + from[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < MOVE_ROWS; ++k) {
+      const int j = j0 + k * TEAMS;
+      if (piece == 2 && j < a.d_out.capacity) a.weights_out[(long long)row * a.d_out.capacity + j] = weight[k];
+      if (from[k] < 0) continue;
+      const int r = j % KV4_BLOCK;
+      // V's words of a place differ by 4 pairs of words, which is 2 pieces
+      const int swap = DH == 64 || piece < C ? 0 : ((from[k] ^ j) & 2);
+      uint8_t* block = dst + (long long)(j / KV4_BLOCK) * L::BYTES;
+      const int at = (piece < C ? 0 : L::V_CODES) + r * L::ROW + ((piece < C ? piece : piece - C) ^ swap) * 16;
+      *reinterpret_cast<uint4*>(block + at) = codes[k];
+      if (piece < 2) {
+#pragma unroll
+        for (int g = 0; g < L::GROUPS; ++g)
+          reinterpret_cast<uint32_t*>(block + (piece == 0 ? L::K_PARAMS : L::V_PARAMS) + r * L::PROW)[g] = params[k][g];
+      }
     }
   }
 }

@@ -296,14 +296,14 @@ int bpt_kv4_store(void* cache, int b, int kv_heads, int capacity, int dh, const 
   a.start = start;
   a.counts = counts;
   BPT_TRY(stream_status_word(st, &a.status));
-  const long long units = (long long)n * kv_heads * (dh / 8);
+  const long long units = (long long)n * kv_heads * (dh / 16);
   const dim3 grid((unsigned)((units + KV4_THREADS - 1) / KV4_THREADS), grid_y(b));
+  const bool wide = aligned(rk, 32) && aligned(rv, 32);  // 32-byte loads
   {
     LaunchScope ls("kv4_store", st);
-    if (dh == 128)
-      kv4_store_kernel<128><<<grid, KV4_THREADS, 0, st>>>(a);
-    else
-      kv4_store_kernel<64><<<grid, KV4_THREADS, 0, st>>>(a);
+    auto kernel = dh == 128 ? (wide ? kv4_store_kernel<128, true> : kv4_store_kernel<128, false>)
+                            : (wide ? kv4_store_kernel<64, true> : kv4_store_kernel<64, false>);
+    kernel<<<grid, KV4_THREADS, 0, st>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
@@ -416,7 +416,7 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   if (weights) {
     LaunchScope ls("kv4_weights", st);
     const Kv4WeightsArgs w{a.scores, a.lse2, weights, a.d, lens, n, heads, a.causal};
-    const dim3 grid((unsigned)((capacity + KVA_THREADS - 1) / KVA_THREADS), grid_y((long long)b * kv_heads));
+    const dim3 grid((unsigned)((capacity / 4 + KVA_THREADS - 1) / KVA_THREADS), grid_y((long long)b * kv_heads));
     BPT_TRY(launch_dependent(kv4_weights_kernel, w, grid, KVA_THREADS, st));
   }
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
@@ -457,18 +457,18 @@ int bpt_kv4_evict(const void* cache, const float* weights, const int* lens, int 
   {
     LaunchScope ls("kv4_select", st);
     const Kv4SelectArgs a{weights, d, lens, keep, recent, kept, lens_out, status};
-    kv4_select_kernel<<<(unsigned)rows, EVICT_THREADS, 0, st>>>(a);
+    if (capacity <= EVICT_CACHED)
+      kv4_select_kernel<true><<<(unsigned)rows, EVICT_THREADS, (size_t)capacity * 4, st>>>(a);
+    else
+      kv4_select_kernel<false><<<(unsigned)rows, EVICT_THREADS, 0, st>>>(a);
   }
   {
     LaunchScope ls("kv4_move", st);
     const Kv4MoveArgs a{reinterpret_cast<const uint8_t*>(cache), reinterpret_cast<uint8_t*>(cache_out), d, d_out,
                         weights, weights_out, kept, lens_out, keep};
-    const int team = dh == 128 ? 8 : 4, per = KV4_THREADS / team;
+    const int per = KV4_THREADS / (dh == 128 ? 8 : 4) * MOVE_ROWS;
     const dim3 grid((unsigned)((capacity_out + per - 1) / per), grid_y((long long)rows));
-    if (dh == 128)
-      kv4_move_kernel<128><<<grid, KV4_THREADS, 0, st>>>(a);
-    else
-      kv4_move_kernel<64><<<grid, KV4_THREADS, 0, st>>>(a);
+    BPT_TRY(launch_dependent(dh == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>, a, grid, KV4_THREADS, st));
   }
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
