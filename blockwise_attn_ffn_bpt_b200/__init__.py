@@ -482,6 +482,12 @@ def _rows(t: torch.Tensor, name: str, width: int, dtypes, like: Optional[torch.T
     return t.data_ptr(), stride[0], stride[1]
 
 
+def _new_rows(like: torch.Tensor, b: int, s: int, width: int) -> tuple:
+    """A new contiguous tensor [b, s, width], the shape of `like`, and its place as of _rows."""
+    t = torch.empty_like(like) if like.is_contiguous() else like.new_empty((b, s, width))
+    return t, (t.data_ptr(), s * width, width)
+
+
 class _On:
     """The tensors' device and the given stream (default: the device's current
     one) as torch's current ones, so that outputs and workspaces belong to the
@@ -527,29 +533,33 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], heads: int, kv_heads: int
     pq = _rows(q, "q", heads * dh, kinds)
     if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous fp64 vector in host memory")
-    pk = pko = (None, 0, 0)
+    pk = (None, 0, 0)
     if k is None:
         kv_heads, k_out = 0, None
     else:
         pk = _rows(k, "k", kv_heads * dh, kinds, q)
     at, size, step = None, 8, 0
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64) or positions.device != q.device:
+        if positions.dtype not in (torch.int32, torch.int64) or positions.get_device() != q.get_device():
             raise TypeError("positions must be int32 or int64 on q's device")
-        if tuple(positions.shape) not in ((b, s), (s,)):
-            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(b, s)} or {(s,)}")
-        if positions.stride(-1) != 1 and s > 1:
+        shape, stride = positions.shape, positions.stride()
+        if shape != (b, s) and shape != (s,):
+            raise ValueError(f"positions has shape {tuple(shape)}, expected {(b, s)} or {(s,)}")
+        if stride[-1] != 1 and s > 1:
             raise ValueError("positions must be contiguous along the sequence")
         at, size = positions.data_ptr(), positions.element_size()
-        step = positions.stride(0) if positions.dim() == 2 else 0
+        step = stride[0] if len(shape) == 2 else 0
     dtype = BPT_DTYPE_F32 if q.dtype == torch.float32 else BPT_DTYPE_BF16
     with _On(q.get_device(), stream) as st:
         if q_out is None:
-            q_out = q.new_empty((b, s, heads * dh))
-        pqo = _rows(q_out, "q_out", heads * dh, kinds, q)
-        if k is not None:
-            if k_out is None:
-                k_out = q.new_empty((b, s, kv_heads * dh))
+            q_out, pqo = _new_rows(q, b, s, heads * dh)
+        else:
+            pqo = _rows(q_out, "q_out", heads * dh, kinds, q)
+        if k is None:
+            pko = (None, 0, 0)
+        elif k_out is None:
+            k_out, pko = _new_rows(k, b, s, kv_heads * dh)
+        else:
             pko = _rows(k_out, "k_out", kv_heads * dh, kinds, q)
         r = lib().bpt_rotary(dtype, *pq, *pk, b, s, heads, kv_heads, dh, 2 * inv_freq.numel(), int(bool(interleaved)),
                              inv_freq.data_ptr(), float(magnitude), at, size, step, int(offset), int(bool(inverse)),
@@ -659,7 +669,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, heads: i
     data, b, kv_heads, capacity, dh = cache._args()
     nbytes = _kv4_workspace_bytes(b, n, heads, kv_heads, capacity, dh, pw is not None)
     with _On(dev.index, stream) as st:
-        o = q.new_empty((b, n, heads * dh))
+        o = _new_rows(q, b, n, heads * dh)[0]
         lse2 = q.new_empty((b, heads, n), dtype=torch.float32) if return_lse else None
         ws = cache.data.new_empty(max(nbytes, 1))
         r = lib().bpt_kv4_attention(*pq, data, pl, b, n, heads, kv_heads, capacity, dh, int(bool(causal)),

@@ -190,9 +190,8 @@ struct Kv4LoadArgs {
 };
 
 // min + scale c of the 8 codes of a word, as bf16.
-__device__ __forceinline__ uint4 kv4_values(uint32_t word, uint32_t params) {
+__device__ __forceinline__ void kv4_values(uint32_t word, uint32_t params, uint32_t* out) {
   const float scale = __uint_as_float(params << 16), lo = __uint_as_float(params & 0xffff0000u);
-  uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // 2^23 + c is exact in fp32, and so is c again
@@ -200,38 +199,60 @@ __device__ __forceinline__ uint4 kv4_values(uint32_t word, uint32_t params) {
     const float c1 = __uint_as_float(((word >> (8 * i + 4)) & 15u) | 0x4b000000u) - 8388608.0f;
     out[i] = pack_bf16x2(fmaf(c0, scale, lo), fmaf(c1, scale, lo));
   }
-  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// The store's mapping the other way round. Bound by HBM (its writes).
-template <int DH>
+// 32 bytes that this kernel does not read again.
+__device__ __forceinline__ void store_stream32(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
+               "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+// The store's mapping the other way round: 16 dimensions of K and V a thread.
+// Bound by HBM (its writes). The outputs' rows are 128 bytes or more, so every
+// 32 bytes are aligned where their start is (WIDE).
+template <int DH, bool WIDE>
 __global__ void __launch_bounds__(KV4_THREADS) kv4_load_kernel(const __grid_constant__ Kv4LoadArgs a) {
-  constexpr int U = DH / 8;
+  constexpr int U = DH / 16;
   using L = Kv4<DH>;
   const unsigned i = blockIdx.x * (unsigned)KV4_THREADS + threadIdx.x;
   const int u = i % U;
   const unsigned rest = i / U;
-  const int t = rest / a.d.kv_heads, head = rest - (unsigned)t * a.d.kv_heads;
+  const int t = rest / (unsigned)a.d.kv_heads, head = rest - (unsigned)t * a.d.kv_heads;
   if (t >= a.n) return;
   for (int beta = blockIdx.y; beta < a.d.b; beta += gridDim.y) {
     const int len = clamp_count(a.lens[beta], a.d.capacity, a.status);
     const long long at = (a.start == nullptr ? 0LL : (long long)a.start[beta]) + t;
     if (at < 0) record_range(a.status);
-    uint4 k = {}, v = {};
+    uint32_t x[2][8] = {};
     if (at >= 0 && at < len) {
       const int r = at % KV4_BLOCK;
       const uint8_t* block =
           a.cache + (((long long)beta * a.d.kv_heads + head) * a.d.blocks() + at / KV4_BLOCK) * L::BYTES;
-      const uint32_t wk = *reinterpret_cast<const uint32_t*>(block + r * L::ROW + kv4_k_place<DH>(u) * 4);
-      const uint32_t wv = *reinterpret_cast<const uint32_t*>(block + L::V_CODES + r * L::ROW + kv4_v_place<DH>(u, r) * 4);
-      const uint32_t pk = *reinterpret_cast<const uint32_t*>(block + L::K_PARAMS + r * L::PROW + u / 8 * 4);
-      const uint32_t pv = *reinterpret_cast<const uint32_t*>(block + L::V_PARAMS + r * L::PROW + u / 8 * 4);
-      k = kv4_values(__funnelshift_r(wk, wk, 3), pk);
-      v = kv4_values(wv, pv);
+      uint32_t word[2][2], params[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        word[0][w] = __ldg(reinterpret_cast<const uint32_t*>(block + r * L::ROW) + kv4_k_place<DH>(2 * u + w));
+        word[1][w] = __ldg(reinterpret_cast<const uint32_t*>(block + L::V_CODES + r * L::ROW) + kv4_v_place<DH>(2 * u + w, r));
+        params[w] = __ldg(reinterpret_cast<const uint32_t*>(block + (w ? L::V_PARAMS : L::K_PARAMS) + r * L::PROW) + u / 4);
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        kv4_values(__funnelshift_r(word[0][w], word[0][w], 3), params[0], x[0] + 4 * w);
+        kv4_values(word[1][w], params[1], x[1] + 4 * w);
+      }
     }
-    const long long to = ((beta * (long long)a.n + t) * a.d.kv_heads + head) * DH + u * 8;
-    *reinterpret_cast<uint4*>(a.x[0] + to) = k;
-    *reinterpret_cast<uint4*>(a.x[1] + to) = v;
+    const long long to = ((beta * (long long)a.n + t) * a.d.kv_heads + head) * DH + u * 16;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if (WIDE) {
+        store_stream32(a.x[w] + to, x[w]);
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(a.x[w] + to);
+        dst[0] = make_uint4(x[w][0], x[w][1], x[w][2], x[w][3]);
+        dst[1] = make_uint4(x[w][4], x[w][5], x[w][6], x[w][7]);
+      }
+    }
   }
 }
 

@@ -333,14 +333,14 @@ int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, c
   a.start = start;
   a.lens = lens;
   BPT_TRY(stream_status_word(st, &a.status));
-  const long long units = (long long)n * kv_heads * (dh / 8);
+  const long long units = (long long)n * kv_heads * (dh / 16);
   const dim3 grid((unsigned)((units + KV4_THREADS - 1) / KV4_THREADS), grid_y(b));
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;  // 32-byte stores
   {
     LaunchScope ls("kv4_load", st);
-    if (dh == 128)
-      kv4_load_kernel<128><<<grid, KV4_THREADS, 0, st>>>(a);
-    else
-      kv4_load_kernel<64><<<grid, KV4_THREADS, 0, st>>>(a);
+    auto kernel = dh == 128 ? (wide ? kv4_load_kernel<128, true> : kv4_load_kernel<128, false>)
+                            : (wide ? kv4_load_kernel<64, true> : kv4_load_kernel<64, false>);
+    kernel<<<grid, KV4_THREADS, 0, st>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
