@@ -169,16 +169,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// (x & mask) | MAGIC in one operation. The mask comes in a register: with two
-// constants the compiler makes two operations of it, and these are what the
-// kernel's arithmetic units spend most of their time on.
-template <uint32_t MAGIC>
-__device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t mask) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "n"(MAGIC));
-  return y;
-}
-
 // The transpose of an 8 x 8 matrix of bf16 held two to a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -262,7 +252,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   const int fold = 2 * t / CW;           // the copy that this lane's two columns of a result belong to
   const int row_fold = F == 1 ? 0 : g / CW;  // the copy that this lane's column of an operand belongs to
   const float lazy = KVA_LAZY / a.score_scale;
-  // zero is 0: values that the compiler does not know, so that they stay in registers
+  // the masks of and_or, which are most of what the arithmetic units do here
   const uint32_t k_mask = 0x00780078u + a.zero, v_mask = 0x000f000fu + a.zero;
   int done = 0;
   while (done < count) {
@@ -333,8 +323,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             uint32_t xa[4], xb[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              xa[e] = code_pair<0x41804180u>(__funnelshift_r(ka[i], ka[i], 4 * e), k_mask);
-              xb[e] = code_pair<0x41804180u>(__funnelshift_r(kb[i], kb[i], 4 * e), k_mask);
+              xa[e] = and_or<0x41804180u>(__funnelshift_r(ka[i], ka[i], 4 * e), k_mask);
+              xb[e] = and_or<0x41804180u>(__funnelshift_r(kb[i], kb[i], 4 * e), k_mask);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -469,8 +459,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
               for (int x = 0; x < 2; ++x) b[nt][x] = F == 1 || row_fold == f ? bf[nt][gi][x] : 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t a0 = code_pair<0x43004300u>(lo0 >> (4 * i), v_mask), a1 = code_pair<0x43004300u>(hi0 >> (4 * i), v_mask);
-              const uint32_t a2 = code_pair<0x43004300u>(lo1 >> (4 * i), v_mask), a3 = code_pair<0x43004300u>(hi1 >> (4 * i), v_mask);
+              const uint32_t a0 = and_or<0x43004300u>(lo0 >> (4 * i), v_mask), a1 = and_or<0x43004300u>(hi0 >> (4 * i), v_mask);
+              const uint32_t a2 = and_or<0x43004300u>(lo1 >> (4 * i), v_mask), a3 = and_or<0x43004300u>(hi1 >> (4 * i), v_mask);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][gi][i], a0, a1, a2, a3, b[nt][0], b[nt][1], o[nt][gi][i]);
             }

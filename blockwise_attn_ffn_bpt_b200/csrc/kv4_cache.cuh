@@ -100,12 +100,17 @@ __device__ __forceinline__ void kv4_quantise(const uint32_t (&raw)[8], uint32_t 
   const float lo = __bfloat162float(lo16);
   const float range = -__high2float(ends) - lo;
   const bool finite = range < __int_as_float(0x7f800000);  // else the group reads back as NaN
-  const __nv_bfloat16 scale16 = __float2bfloat16_rn(__fdiv_rn(range, 15.0f));
+  // range / 15: a product with the rounded reciprocal, corrected by its exact
+  // residual (Markstein 1990), which leaves the correctly rounded quotient
+  constexpr float fifteenth = 1.0f / 15.0f;
+  const float q = range * fifteenth;
+  const __nv_bfloat16 scale16 = __float2bfloat16_rn(fmaf(fmaf(-15.0f, q, range), fifteenth, q));
   const float scale = __bfloat162float(scale16);
   const bool live = finite && scale >= 1.17549435e-38f;
-  const float r = live ? __fdiv_rn(1.0f, scale) : 0.0f;
+  const float r = live ? __frcp_rn(scale) : 0.0f;
   params = !finite ? 0x7fc00000u
                    : (live ? (uint32_t)__bfloat16_as_ushort(scale16) : 0u) | ((uint32_t)__bfloat16_as_ushort(lo16) << 16);
+  const uint64_t minus = f2_pack(-lo, -lo), times = f2_pack(r, r), magic = f2_pack(12582912.0f, 12582912.0f);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     // Adding 1.5 * 2^23 rounds the exact product to a whole number, ties to
@@ -114,9 +119,12 @@ __device__ __forceinline__ void kv4_quantise(const uint32_t (&raw)[8], uint32_t 
     uint32_t sum = 0;
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
-      const float2 f = __bfloat1622float2(x[4 * w + i]);
-      sum = sum * 16u + __float_as_uint(fmaf(f.y - lo, r, 12582912.0f));
-      sum = sum * 16u + __float_as_uint(fmaf(f.x - lo, r, 12582912.0f));
+      const uint32_t two = raw[4 * w + i];
+      float lo_code, hi_code;
+      f2_unpack(f2_fma(f2_add(f2_pack(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u)), minus), times, magic),
+                lo_code, hi_code);
+      sum = sum * 16u + __float_as_uint(hi_code);
+      sum = sum * 16u + __float_as_uint(lo_code);
     }
     word[w] = live ? sum - 0x4b400000u * 0x11111111u : 0u;
   }
@@ -187,17 +195,31 @@ struct Kv4LoadArgs {
   const int* start;     // [b], or null: 0
   const int* lens;      // [b]: tokens at or past it read as zero
   int* status;
+  uint32_t zero;        // 0
 };
 
-// min + scale c of the 8 codes of a word, as bf16.
-__device__ __forceinline__ void kv4_values(uint32_t word, uint32_t params, uint32_t* out) {
+// (x & mask) | MAGIC in one operation. The mask comes in a register that the
+// compiler does not know (a kernel argument is part of it): with two constants
+// it makes two operations.
+template <uint32_t MAGIC>
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "n"(MAGIC));
+  return y;
+}
+
+// min + scale c of the 8 codes of a word, as bf16. mask: 15.
+__device__ __forceinline__ void kv4_values(uint32_t word, uint32_t params, uint32_t mask, uint32_t* out) {
   const float scale = __uint_as_float(params << 16), lo = __uint_as_float(params & 0xffff0000u);
+  const uint64_t minus = f2_pack(-8388608.0f, -8388608.0f), times = f2_pack(scale, scale), plus = f2_pack(lo, lo);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // 2^23 + c is exact in fp32, and so is c again
-    const float c0 = __uint_as_float(((word >> (8 * i)) & 15u) | 0x4b000000u) - 8388608.0f;
-    const float c1 = __uint_as_float(((word >> (8 * i + 4)) & 15u) | 0x4b000000u) - 8388608.0f;
-    out[i] = pack_bf16x2(fmaf(c0, scale, lo), fmaf(c1, scale, lo));
+    const uint64_t c = f2_add(f2_pack(__uint_as_float(and_or<0x4b000000u>(word >> (8 * i), mask)),
+                                      __uint_as_float(and_or<0x4b000000u>(word >> (8 * i + 4), mask))), minus);
+    float x0, x1;
+    f2_unpack(f2_fma(c, times, plus), x0, x1);
+    out[i] = pack_bf16x2(x0, x1);
   }
 }
 
@@ -238,8 +260,8 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_load_kernel(const __grid_cons
       }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        kv4_values(__funnelshift_r(word[0][w], word[0][w], 3), params[0], x[0] + 4 * w);
-        kv4_values(word[1][w], params[1], x[1] + 4 * w);
+        kv4_values(__funnelshift_r(word[0][w], word[0][w], 3), params[0], 15u + a.zero, x[0] + 4 * w);
+        kv4_values(word[1][w], params[1], 15u + a.zero, x[1] + 4 * w);
       }
     }
     const long long to = ((beta * (long long)a.n + t) * a.d.kv_heads + head) * DH + u * 16;

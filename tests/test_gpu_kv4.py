@@ -88,6 +88,18 @@ def test_store_writes_the_oracles_bytes_and_no_others(kv, n, dh):
             assert (block[rest] == 0xA5).all()
 
 
+def test_store_at_every_scale():
+    # down to where the scale is no normal number, and whole numbers, whose quotients tie
+    rng = np.random.default_rng(0)
+    for e in [*range(-133, 120, 9), -126, -125, -122, -120]:
+        for x in (rng.standard_normal((1, 64, 128)) * 2.0 ** e, rng.integers(-16, 17, (1, 64, 128)) * 2.0 ** e):
+            k = torch.tensor(x).float().bfloat16().cuda()
+            cache = bpt.kv4_cache(1, 1, 64, 128)
+            bpt.kv4_store(cache, k, k, ints(0))
+            kn = heads_of(k, 1)[0, :, 0]
+            assert np.array_equal(cache.data[0, 0].cpu().numpy(), so.pack(kn, kn)[0])
+
+
 def test_load_returns_the_values_and_zeros_past_the_length():
     for dh in (64, 128):
         lens = [70, 3, 0]
@@ -164,7 +176,7 @@ def check_attention(q, cache, held, lens, heads, causal=True, weights=None, **kw
         # the bounds of the module's comment
         big = np.repeat(np.abs(one["km"]) + 31 * one["ks"], 64, -1)              # [kv, len, dh]
         E = (dh + 16) * 2.0 ** -24 * c * np.einsum("nhd,hud->hnu", np.abs(qn[i]), big[hh]).max(-1)  # [heads, n]
-        assert (np.abs(ln[i] - rl)[live] <= (E + 2.0 ** -20 + 2.0 ** -23 * np.abs(rl))[live]).all()
+        assert (np.abs(ln[i][live] - rl[live]) <= (E + 2.0 ** -20 + 2.0 ** -23 * np.abs(rl))[live]).all()
         s = np.einsum("nhd,hud->hnu", qn[i], one["k"][hh]) / np.sqrt(dh)
         seen = np.arange(lens[i]) < (lens[i] - n + 1 + np.arange(n) if causal else np.full(n, lens[i]))[:, None]
         p = np.where(seen, np.exp2(s * np.log2(np.e) - np.where(live, rl, 0)[..., None]), 0)  # [heads, n, len]
