@@ -79,15 +79,20 @@ __device__ __forceinline__ int kv4_seen(int len, int n, int t, int causal) {
 }
 
 // The even split. Segments are (sequence, head, block of columns) in that
-// order, T blocks of 64 tokens in all; warp w of W takes blocks T w / W up to T
-// (w + 1) / W, and its result for segment s goes to slot s + w (both grow along
-// the run, so no two share one).
+// order, `total` blocks of 64 tokens in all (below 2^31); the first total %
+// warps warps take one block more than the others. The result of warp w for
+// segment s goes to slot s + w (both grow along the run, so no two share one).
 struct KvaSplit {
-  long long total;
-  int warps;
-  __device__ __forceinline__ long long first(int w) const { return total * w / warps; }
-  __device__ __forceinline__ int warp_of(long long block) const {
-    return (int)(((block + 1) * warps - 1) / total);
+  uint32_t total, warps, each, rest;
+  __device__ __forceinline__ KvaSplit(uint32_t t, uint32_t max_warps) : total(t) {
+    warps = max(1u, min(t, max_warps));
+    each = t / warps;
+    rest = t - each * warps;
+  }
+  __device__ __forceinline__ uint32_t first(uint32_t w) const { return each * w + min(w, rest); }
+  __device__ __forceinline__ uint32_t warp_of(uint32_t block) const {
+    const uint32_t longer = (each + 1) * rest;
+    return block < longer ? block / (each + 1) : rest + (block - longer) / each;
   }
 };
 
@@ -96,21 +101,16 @@ __device__ __forceinline__ int kva_blocks(const Kv4AttnArgs& a, int beta) {
 }
 
 // Called by a whole warp: the split, and the blocks before sequence `beta`.
-__device__ __forceinline__ KvaSplit kva_split(const Kv4AttnArgs& a, int beta, long long& before) {
-  const long long per = (long long)a.d.kv_heads * a.blocks_of_cols;
-  long long total = 0, prior = 0;
+__device__ __forceinline__ KvaSplit kva_split(const Kv4AttnArgs& a, int beta, uint32_t& before) {
+  const uint32_t per = (uint32_t)a.d.kv_heads * a.blocks_of_cols;
+  uint32_t total = 0, prior = 0;
   for (int i = lane_id(); i < a.d.b; i += 32) {
-    const int nb = kva_blocks(a, i);
+    const uint32_t nb = kva_blocks(a, i);
     total += nb;
     if (i < beta) prior += nb;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    prior += __shfl_xor_sync(0xffffffffu, prior, o);
-  }
-  before = prior * per;
-  return KvaSplit{total * per, (int)max(1LL, min(total * per, (long long)a.max_warps))};
+  before = __reduce_add_sync(0xffffffffu, prior) * per;
+  return KvaSplit(__reduce_add_sync(0xffffffffu, total) * per, (uint32_t)a.max_warps);
 }
 
 // A place in the run: block `blk` of row `row` (head and block of columns) of
@@ -130,23 +130,23 @@ struct KvaPlace {
 };
 
 // The place of block t (whole warp).
-__device__ __forceinline__ KvaPlace kva_find(const Kv4AttnArgs& a, long long t, int rows) {
-  long long base = 0;
+__device__ __forceinline__ KvaPlace kva_find(const Kv4AttnArgs& a, uint32_t t, int rows) {
+  uint32_t base = 0;
   const int lane = lane_id();
   for (int b0 = 0; b0 < a.d.b; b0 += 32) {
-    const int nb = b0 + lane < a.d.b ? kva_blocks(a, b0 + lane) : 0;
-    long long sum = (long long)nb * rows;
+    const uint32_t nb = b0 + lane < a.d.b ? kva_blocks(a, b0 + lane) : 0;
+    uint32_t sum = nb * rows;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += x;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, base + sum > t);
     if (past) {
       const int src = __ffs(past) - 1;
-      const int n = __shfl_sync(0xffffffffu, nb, src);
-      const long long r = t - (base + __shfl_sync(0xffffffffu, sum, src) - (long long)n * rows);
-      return KvaPlace{b0 + src, (int)(r / n), (int)(r % n), n};
+      const uint32_t n = __shfl_sync(0xffffffffu, nb, src);
+      const uint32_t r = t - (base + __shfl_sync(0xffffffffu, sum, src) - n * rows), row = r / n;
+      return KvaPlace{b0 + src, (int)row, (int)(r - row * n), (int)n};
     }
     base += __shfl_sync(0xffffffffu, sum, 31);
   }
@@ -221,14 +221,15 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   __syncthreads();
   const Abort ab{flag, a.status};
 
-  long long unused;
+  uint32_t unused;
   const KvaSplit split = kva_split(a, 0, unused);
   const int rows = a.d.kv_heads * a.blocks_of_cols;
   if (blockIdx.x == 0 && warp == 0)
     for (int i = lane; i < a.d.b; i += 32) clamp_count(a.lens[i], a.d.capacity, a.status);
+  const int group = a.heads / a.d.kv_heads;
   const int w = warp * gridDim.x + blockIdx.x;  // neighbours of a run on different SMs
-  if (w >= split.warps || split.total == 0) return;
-  const long long t0 = split.first(w);
+  if (w >= (int)split.warps || split.total == 0) return;
+  const uint32_t t0 = split.first(w);
   const int count = (int)(split.first(w + 1) - t0);
   KvaPlace at = kva_find(a, t0, rows), next = at;
 
@@ -246,14 +247,17 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
     ++next.blk;
     next.settle(a, rows);
   };
-  for (int i = 0; i < C::STAGES; ++i) issue();
-
-  const int group = a.heads / a.d.kv_heads;
   const int fold = 2 * t / CW;           // the copy that this lane's two columns of a result belong to
   const int row_fold = F == 1 ? 0 : g / CW;  // the copy that this lane's column of an operand belongs to
   const float lazy = KVA_LAZY / a.score_scale;
   // the masks of and_or, which are most of what the arithmetic units do here
   const uint32_t k_mask = 0x00780078u + a.zero, v_mask = 0x000f000fu + a.zero;
+  // where this lane's words and parameters lie in a block, the compile-time
+  // parts left out (8 rows on, V's words lie in the same order)
+  const uint32_t k_at = kva_token(g) * L::ROW + t * (L::ROW / 4);
+  const uint32_t v_at[2] = {L::V_CODES + t * L::ROW + kv4_v_place<DH>(g, t) * 4u,
+                            L::V_CODES + (7 - t) * L::ROW + kv4_v_place<DH>(g, 7 - t) * 4u};
+  const int token = fold * 16 + kva_token(g);  // of this lane's results: 16 F j + token, and 8 on
   int done = 0;
   while (done < count) {
     // one segment's part of the run
@@ -263,16 +267,25 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
     uint32_t qf[NT][F][KW][4];
     float qs[NT][G][2], init[NT][G][4];
     int lim[NT][2];
+    uint4 raw[NT][KW];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int col = col0 + nt * 8 + g % CW;
       const bool real = col < a.cols;
       const int tok = real ? col / group : 0, head = kvh * group + (real ? col - tok * group : 0);
       const __nv_bfloat16* q = a.q + at.beta * a.bs_q + tok * a.ld_q + (long long)head * DH;
+#pragma unroll
+      for (int i = 0; i < KW; ++i)
+        raw[nt][i] = real ? *reinterpret_cast<const uint4*>(q + (i * 4 + t) * 8) : make_uint4(0, 0, 0, 0);
+    }
+    if (issued == 0)  // the first blocks, behind the queries: those would wait for all of them
+      for (int i = 0; i < C::STAGES; ++i) issue();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       float sum[G] = {};
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
-        const uint4 x = real ? *reinterpret_cast<const uint4*>(q + (i * 4 + t) * 8) : make_uint4(0, 0, 0, 0);
+        const uint4 x = raw[nt][i];
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[i / 2] += scale_of(y[e]) + min_of(y[e]);
@@ -301,7 +314,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
     // m: the maximum's reference, in units of a score before score_scale; the
     // sums of a lane are of its own tokens until the end of the run
     float o[NT][G][4][4] = {}, ones[NT][G][4] = {};
-    float m[NT][2], l[NT][2] = {}, off[NT][G][2] = {};
+    float m[NT][2], ref[NT][2] = {}, l[NT][2] = {}, off[NT][G][2] = {};  // ref: m score_scale, or 0 for none
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
 
@@ -314,10 +327,9 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         float acc[NT][G][4];
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-          const int ra = (j * F + f) * 16 + kva_token(g);
           uint32_t ka[KW], kb[KW];
-          lds(blk + ra * L::ROW + t * (L::ROW / 4), ka);
-          lds(blk + (ra + 8) * L::ROW + t * (L::ROW / 4), kb);
+          lds(blk + k_at + (j * F + f) * 16 * L::ROW, ka);
+          lds(blk + k_at + ((j * F + f) * 16 + 8) * L::ROW, kb);
 #pragma unroll
           for (int i = 0; i < KW; ++i) {
             uint32_t xa[4], xb[4];
@@ -335,7 +347,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             }
           }
         }
-        const int ra = (j * F + fold) * 16 + kva_token(g);  // the tokens of this lane's results: ra and ra + 8
+        const int ra = j * F * 16 + token;
         uint32_t pa[G], pb[G];
         lds(blk + L::K_PARAMS + ra * L::PROW, pa);
         lds(blk + L::K_PARAMS + (ra + 8) * L::PROW, pb);
@@ -354,7 +366,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
           }
       }
       if (a.scores != nullptr) {
-        float* to = a.scores + ((long long)at.beta * a.d.kv_heads + kvh) * a.cols * a.d.capacity + key0 + kva_token(g);
+        float* to = a.scores + ((long long)at.beta * a.d.kv_heads + kvh) * a.cols * a.d.capacity + key0 + token;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -363,7 +375,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             if (col < a.cols)
 #pragma unroll
               for (int j = 0; j < J; ++j)
-                to[(long long)col * a.d.capacity + (j * F + fold) * 16 + (e >> 1) * 8] = s[j][nt][e] * a.score_scale;
+                to[(long long)col * a.d.capacity + j * F * 16 + (e >> 1) * 8] = s[j][nt][e] * a.score_scale;
           }
       }
 
@@ -391,6 +403,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
               now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
             const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx((m[nt][e] - now) * a.score_scale);
             m[nt][e] = now;
+            ref[nt][e] = now == -INFINITY ? 0.f : now * a.score_scale;
             l[nt][e] *= f;
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) {
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const int ra = (j * F + fold) * 16 + kva_token(g);
+        const int ra = j * F * 16 + token;
         uint32_t va[G], vb[G];
         lds(blk + L::V_PARAMS + ra * L::PROW, va);
         lds(blk + L::V_PARAMS + (ra + 8) * L::PROW, vb);
@@ -417,8 +430,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1] * a.score_scale;
-            p[e] = ex2_approx(fmaf(s[j][nt][e], a.score_scale, -ref));
+            p[e] = ex2_approx(fmaf(s[j][nt][e], a.score_scale, -ref[nt][e & 1]));
             l[nt][e & 1] += p[e];
           }
 #pragma unroll
@@ -445,8 +457,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
           uint32_t v[4][G];  // this lane's words of four tokens
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int r = (j * F + f) * 16 + (x >> 1) * 8 + ((x & 1) ? 7 - t : t);
-            lds(blk + L::V_CODES + r * L::ROW + kv4_v_place<DH>(g, r) * 4, v[x]);
+            lds(blk + v_at[x & 1] + ((j * F + f) * 16 + (x >> 1) * 8) * L::ROW, v[x]);
           }
 #pragma unroll
           for (int gi = 0; gi < G; ++gi) {
@@ -580,12 +591,12 @@ __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_c
   grid_dependents_start();
   bool waited = false;
   for (int beta = blockIdx.y; beta < a.d.b; beta += gridDim.y) {
-    long long before;
+    uint32_t before;
     const KvaSplit split = kva_split(a, beta, before);
     const int nb = kva_blocks(a, beta), row = kvh * a.blocks_of_cols + cb;
     int w0 = 0, w1 = -1;
     if (nb > 0) {
-      const long long first = before + (long long)row * nb;
+      const uint32_t first = before + (uint32_t)row * nb;
       w0 = split.warp_of(first);
       w1 = split.warp_of(first + nb - 1);
     }
