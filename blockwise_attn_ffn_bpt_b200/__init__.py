@@ -489,22 +489,22 @@ def _new_rows(like: torch.Tensor, b: int, s: int, width: int) -> tuple:
 
 
 class _On:
-    """The tensors' device and the given stream (default: the device's current
-    one) as torch's current ones, so that outputs and workspaces belong to the
-    stream that uses them. Enters as the stream's handle."""
+    """The given stream's device and stream as torch's current ones, so that
+    outputs and workspaces belong to the stream that uses them; by default the
+    tensors' device and its current stream. Enters as the stream's handle."""
 
-    __slots__ = ("index", "stream", "ctx")
+    __slots__ = ("index", "ctx")
 
     def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
-        if stream is not None and stream.device.index != index:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
-        self.index, self.stream, self.ctx = index, stream, None
+        self.index, self.ctx = index, None
+        if stream is not None:
+            if stream.device.index != index:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+            self.ctx = torch.cuda.stream(stream)
+        elif index != torch._C._cuda_getDevice():
+            self.ctx = torch.cuda.device(index)
 
     def __enter__(self) -> int:
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-        elif self.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.index)
         if self.ctx is not None:
             self.ctx.__enter__()
         return torch._C._cuda_getCurrentRawStream(self.index)
@@ -640,8 +640,8 @@ def kv4_load(cache: KV4Cache, lens: torch.Tensor, n: int, start: Optional[torch.
     ps = None if start is None else cache._ints(start, "start")
     dev = cache.data.device
     with _On(dev.index, stream) as st:
-        shape = (cache.b, n, cache.kv_heads * cache.dh)
-        k, v = cache.data.new_empty(shape, dtype=torch.bfloat16), cache.data.new_empty(shape, dtype=torch.bfloat16)
+        k = cache.data.new_empty((cache.b, n, cache.kv_heads * cache.dh), dtype=torch.bfloat16)
+        v = torch.empty_like(k)
         r = lib().bpt_kv4_load(*cache._args(), ps, pl, n, k.data_ptr(), v.data_ptr(), st)
     _check(r, "bpt_kv4_load")
     return k, v

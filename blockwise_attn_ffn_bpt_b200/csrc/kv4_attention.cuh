@@ -37,6 +37,10 @@ namespace bpt {
 
 constexpr int KVA_THREADS = 256;
 constexpr int KVA_MAX_SMS = 148;      // the split does not grow past it (workspaces are sized without a device)
+// Blocks that the start of a segment takes as long as (KvaSplit). Measured at 16
+// contexts of 4096 tokens, 32 heads of 128: 62.1 us with 0, 61.3 with 1, 61.9
+// with 2; at 8 of 32768 tokens 200.7, 198.8 and 199.9.
+constexpr int KVA_SWITCH = 1;
 constexpr float KVA_LAZY = 8.0f;      // the maximum is raised when a score passes it by this (log2)
 
 // Warps of an SM and stages of a warp: the rings take 216 KB in every case, and
@@ -79,9 +83,13 @@ __device__ __forceinline__ int kv4_seen(int len, int n, int t, int causal) {
 }
 
 // The even split. Segments are (sequence, head, block of columns) in that
-// order, `total` blocks of 64 tokens in all (below 2^31); the first total %
-// warps warps take one block more than the others. The result of warp w for
-// segment s goes to slot s + w (both grow along the run, so no two share one).
+// order. A segment of nb > 0 blocks of 64 tokens counts nb + KVA_SWITCH units:
+// the first ones stand for the start of a segment (its queries, and the sums of
+// the one before), which takes a warp about as long as that many blocks. The
+// `total` units of all segments (below 2^31) are cut into one run a warp; the
+// first total % warps ones have one unit more than the others. The result of
+// warp w for segment s goes to slot s + w (both grow along the run, so no two
+// share one).
 struct KvaSplit {
   uint32_t total, warps, each, rest;
   __device__ __forceinline__ KvaSplit(uint32_t t, uint32_t max_warps) : total(t) {
@@ -100,42 +108,48 @@ __device__ __forceinline__ int kva_blocks(const Kv4AttnArgs& a, int beta) {
   return (min(max(a.lens[beta], 0), a.d.capacity) + KV4_BLOCK - 1) / KV4_BLOCK;
 }
 
-// Called by a whole warp: the split, and the blocks before sequence `beta`.
+// Called by a whole warp: the split, and the units before sequence `beta`.
 __device__ __forceinline__ KvaSplit kva_split(const Kv4AttnArgs& a, int beta, uint32_t& before) {
   const uint32_t per = (uint32_t)a.d.kv_heads * a.blocks_of_cols;
   uint32_t total = 0, prior = 0;
   for (int i = lane_id(); i < a.d.b; i += 32) {
     const uint32_t nb = kva_blocks(a, i);
-    total += nb;
-    if (i < beta) prior += nb;
+    const uint32_t units = nb ? nb + KVA_SWITCH : 0;
+    total += units;
+    if (i < beta) prior += units;
   }
   before = __reduce_add_sync(0xffffffffu, prior) * per;
   return KvaSplit(__reduce_add_sync(0xffffffffu, total) * per, (uint32_t)a.max_warps);
 }
 
-// A place in the run: block `blk` of row `row` (head and block of columns) of
-// sequence beta, which has nb blocks.
+// A place in a run: block `blk` of row `row` (head and block of columns) of
+// sequence beta, which has nb blocks; `left` units of the run from there on.
 struct KvaPlace {
-  int beta, row, blk, nb;
-  __device__ __forceinline__ void settle(const Kv4AttnArgs& a, int rows) {
-    while (blk >= nb && beta < a.d.b) {
-      blk = 0;
-      if (nb == 0 || ++row == rows) {
-        row = 0;
-        ++beta;
-        nb = beta < a.d.b ? kva_blocks(a, beta) : 0;
-      }
+  int beta, row, blk, nb, left;
+  // Takes n blocks; at the end of a segment, on to the next one.
+  __device__ __forceinline__ void advance(const Kv4AttnArgs& a, int rows, int n) {
+    blk += n;
+    left -= n;
+    if (blk < nb || left <= 0) return;
+    blk = 0;
+    if (++row == rows) {
+      row = 0;
+      do ++beta;
+      while (beta < a.d.b && (nb = kva_blocks(a, beta)) == 0);
+      if (beta == a.d.b) left = 0;
     }
+    left -= KVA_SWITCH;
   }
 };
 
-// The place of block t (whole warp).
-__device__ __forceinline__ KvaPlace kva_find(const Kv4AttnArgs& a, uint32_t t, int rows) {
+// The place of unit t, and the run of n units from there (whole warp).
+__device__ __forceinline__ KvaPlace kva_find(const Kv4AttnArgs& a, uint32_t t, int n, int rows) {
   uint32_t base = 0;
   const int lane = lane_id();
   for (int b0 = 0; b0 < a.d.b; b0 += 32) {
     const uint32_t nb = b0 + lane < a.d.b ? kva_blocks(a, b0 + lane) : 0;
-    uint32_t sum = nb * rows;
+    const uint32_t units = nb ? (nb + KVA_SWITCH) * rows : 0;
+    uint32_t sum = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
@@ -144,13 +158,14 @@ __device__ __forceinline__ KvaPlace kva_find(const Kv4AttnArgs& a, uint32_t t, i
     const uint32_t past = __ballot_sync(0xffffffffu, base + sum > t);
     if (past) {
       const int src = __ffs(past) - 1;
-      const uint32_t n = __shfl_sync(0xffffffffu, nb, src);
-      const uint32_t r = t - (base + __shfl_sync(0xffffffffu, sum, src) - n * rows), row = r / n;
-      return KvaPlace{b0 + src, (int)row, (int)(r - row * n), (int)n};
+      const uint32_t blocks = __shfl_sync(0xffffffffu, nb, src);
+      const uint32_t r = t - (base + __shfl_sync(0xffffffffu, sum - units, src)), row = r / (blocks + KVA_SWITCH);
+      const int unit = r - row * (blocks + KVA_SWITCH), start = max(KVA_SWITCH - unit, 0);
+      return KvaPlace{b0 + src, (int)row, max(unit - KVA_SWITCH, 0), (int)blocks, n - start};
     }
     base += __shfl_sync(0xffffffffu, sum, 31);
   }
-  return KvaPlace{a.d.b, 0, 0, 0};
+  return KvaPlace{a.d.b, 0, 0, 0, 0};
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -230,12 +245,11 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   const int w = warp * gridDim.x + blockIdx.x;  // neighbours of a run on different SMs
   if (w >= (int)split.warps || split.total == 0) return;
   const uint32_t t0 = split.first(w);
-  const int count = (int)(split.first(w + 1) - t0);
-  KvaPlace at = kva_find(a, t0, rows), next = at;
+  KvaPlace at = kva_find(a, t0, (int)(split.first(w + 1) - t0), rows), next = at;
 
   int issued = 0;
   auto issue = [&]() {  // the next block of the run into its stage
-    if (issued >= count) return;
+    if (next.left <= 0) return;
     if (lane == 0) {
       const uint32_t bar = bars + issued % C::STAGES * 8;
       const uint8_t* src =
@@ -244,8 +258,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       bulk_load(ring + issued % C::STAGES * L::BYTES, src, L::BYTES, bar);
     }
     ++issued;
-    ++next.blk;
-    next.settle(a, rows);
+    next.advance(a, rows, 1);
   };
   const int fold = 2 * t / CW;           // the copy that this lane's two columns of a result belong to
   const int row_fold = F == 1 ? 0 : g / CW;  // the copy that this lane's column of an operand belongs to
@@ -259,7 +272,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
                             L::V_CODES + (7 - t) * L::ROW + kv4_v_place<DH>(g, 7 - t) * 4u};
   const int token = fold * 16 + kva_token(g);  // of this lane's results: 16 F j + token, and 8 on
   int done = 0;
-  while (done < count) {
+  while (at.left > 0) {
     // one segment's part of the run
     const int len = min(max(a.lens[at.beta], 0), a.d.capacity);
     const int kvh = at.row / a.blocks_of_cols, cb = at.row - kvh * a.blocks_of_cols;
@@ -480,7 +493,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       }
     };
 
-    const int piece = min(at.nb - at.blk, count - done);
+    const int piece = min(at.nb - at.blk, at.left);
     for (int k = 0; k < piece; ++k) {
       const int stage = done % C::STAGES;
       if (!warp_wait(bars + stage * 8, (done / C::STAGES) & 1, ab)) {
@@ -539,8 +552,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
           }
         }
       }
-    at.blk += piece;
-    at.settle(a, rows);
+    at.advance(a, rows, piece);
   }
 }
 
@@ -596,7 +608,7 @@ __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_c
     const int nb = kva_blocks(a, beta), row = kvh * a.blocks_of_cols + cb;
     int w0 = 0, w1 = -1;
     if (nb > 0) {
-      const uint32_t first = before + (uint32_t)row * nb;
+      const uint32_t first = before + (uint32_t)row * (nb + KVA_SWITCH) + KVA_SWITCH;
       w0 = split.warp_of(first);
       w1 = split.warp_of(first + nb - 1);
     }

@@ -145,7 +145,8 @@ int check_kv4_attention(int b, int n, int heads, int kv_heads, int capacity, int
   if ((long long)b * n * heads > 0x7fffffffLL) return BPT_ERR_SHAPE;
   if ((double)b * n * heads * capacity > 1e18) return BPT_ERR_SHAPE;
   const int cols = heads / kv_heads * n, pass = 8 * kva_col_blocks(cols);
-  if ((double)b * kv_heads * ((cols + pass - 1) / pass) * (capacity / KV4_BLOCK) > 2147483647.0) return BPT_ERR_SHAPE;
+  if ((double)b * kv_heads * ((cols + pass - 1) / pass) * (capacity / KV4_BLOCK + KVA_SWITCH) > 2147483647.0)
+    return BPT_ERR_SHAPE;
   return BPT_OK;
 }
 
