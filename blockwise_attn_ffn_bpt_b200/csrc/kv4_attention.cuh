@@ -35,7 +35,6 @@
 
 namespace bpt {
 
-constexpr int KVA_THREADS = 256;
 constexpr int KVA_MAX_SMS = 148;      // the split does not grow past it (workspaces are sized without a device)
 // Blocks that the start of a segment takes as long as (KvaSplit). Measured at 16
 // contexts of 4096 tokens, 32 heads of 128: 62.1 us with 0, 61.3 with 1, 61.9
@@ -681,37 +680,69 @@ struct Kv4WeightsArgs {
 };
 
 // weights[u] += sum over the queries that share u's head of 2^(score - lse2):
-// 4 cached tokens a thread. Bound by memory (the scores come from L2 where they
-// fit).
-__global__ void __launch_bounds__(KVA_THREADS) kv4_weights_kernel(const __grid_constant__ Kv4WeightsArgs a) {
+// KVW_VECTORS times 4 cached tokens a thread. Bound by the latency of its reads
+// (the scores come from L2 where they fit): what does not wait for the kernels
+// ahead is read before they end, the scores of two queries at a time after.
+constexpr int KVW_THREADS = 128;
+constexpr int KVW_VECTORS = 2;
+
+__global__ void __launch_bounds__(KVW_THREADS, 8) kv4_weights_kernel(const __grid_constant__ Kv4WeightsArgs a) {
+  constexpr int V = KVW_VECTORS, STEP = KVW_THREADS * 4;
   const int group = a.heads / a.d.kv_heads, cols = group * a.n;
-  const int key = (blockIdx.x * KVA_THREADS + threadIdx.x) * 4;
+  const int key = blockIdx.x * STEP * V + threadIdx.x * 4;
   const int rows = a.d.b * a.d.kv_heads;
-  grid_dependency_wait();
-  if (key >= a.d.capacity) return;
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     const int beta = row / a.d.kv_heads, kvh = row - beta * a.d.kv_heads;
+    float* to = a.weights + (long long)row * a.d.capacity;
+    float4 old[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (key + v * STEP < a.d.capacity) old[v] = *reinterpret_cast<const float4*>(to + key + v * STEP);
     const int len = min(max(a.lens[beta], 0), a.d.capacity);
+    grid_dependency_wait();
     if (key >= len) continue;
     const float* s = a.scores + (long long)row * cols * a.d.capacity + key;
-    float4* to = reinterpret_cast<float4*>(a.weights + (long long)row * a.d.capacity + key);
-    const float4 old = *to;  // past the length nothing is added
-    float sum[4] = {};
-#pragma unroll 4
-    for (int c = 0; c < cols; ++c) {
-      const int t = c / group, head = kvh * group + c - t * group;
-      const int seen = kv4_seen(len, a.n, t, a.causal);
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(s + (long long)c * a.d.capacity));
-      const float lse2 = a.lse2[((long long)beta * a.heads + head) * a.n + t];
-      const float v[4] = {x.x, x.y, x.z, x.w};
+    const float* lse2 = a.lse2 + ((long long)beta * a.heads + kvh * group) * a.n;
+    float sum[V][4] = {};
+    int t = 0, h = 0;  // token and head of the next query
+    for (int c = 0; c < cols; c += 2) {
+      float4 x[2][V];
+      float l[2];
+      int seen[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] += key + e < seen ? ex2_approx(v[e] - lse2) : 0.f;
+      for (int k = 0; k < 2; ++k) {
+        seen[k] = 0;
+        if (c + k < cols) {
+          seen[k] = kv4_seen(len, a.n, t, a.causal);
+          l[k] = __ldcg(lse2 + h * a.n + t);
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (key + v * STEP < len) x[k][v] = __ldcs(reinterpret_cast<const float4*>(s + (long long)(c + k) * a.d.capacity + v * STEP));
+          if (++h == group) {
+            h = 0;
+            ++t;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int at = key + v * STEP;
+          if (at < seen[k]) sum[v][0] += ex2_approx(x[k][v].x - l[k]);
+          if (at + 1 < seen[k]) sum[v][1] += ex2_approx(x[k][v].y - l[k]);
+          if (at + 2 < seen[k]) sum[v][2] += ex2_approx(x[k][v].z - l[k]);
+          if (at + 3 < seen[k]) sum[v][3] += ex2_approx(x[k][v].w - l[k]);
+        }
     }
-    const float w[4] = {old.x, old.y, old.z, old.w};
-    float now[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) now[e] = key + e < len ? w[e] + sum[e] : w[e];
-    *to = make_float4(now[0], now[1], now[2], now[3]);
+    for (int v = 0; v < V; ++v) {
+      const int at = key + v * STEP;
+      if (at < len)  // past the length nothing changes
+        *reinterpret_cast<float4*>(to + at) = make_float4(old[v].x + sum[v][0], at + 1 < len ? old[v].y + sum[v][1] : old[v].y,
+                                                          at + 2 < len ? old[v].z + sum[v][2] : old[v].z,
+                                                          at + 3 < len ? old[v].w + sum[v][3] : old[v].w);
+    }
   }
 }
 

@@ -419,8 +419,9 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   if (weights) {
     LaunchScope ls("kv4_weights", st);
     const Kv4WeightsArgs w{a.scores, a.lse2, weights, a.d, lens, n, heads, a.causal};
-    const dim3 grid((unsigned)((capacity / 4 + KVA_THREADS - 1) / KVA_THREADS), grid_y((long long)b * kv_heads));
-    BPT_TRY(launch_dependent(kv4_weights_kernel, w, grid, KVA_THREADS, st));
+    const int per = KVW_THREADS * 4 * KVW_VECTORS;
+    const dim3 grid((unsigned)((capacity + per - 1) / per), grid_y((long long)b * kv_heads));
+    BPT_TRY(launch_dependent(kv4_weights_kernel, w, grid, KVW_THREADS, st));
   }
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
