@@ -15,6 +15,9 @@ namespace bpt {
 
 constexpr int EVICT_THREADS = 1024;
 constexpr int EVICT_BINS = 2048;
+// Copies of the histogram, one to every fourth lane: weights of a few octaves
+// share few bins of the first digit, and lanes that add to one bin take turns.
+constexpr int EVICT_COPIES = 4;
 constexpr int EVICT_CACHED = 49152;  // tokens whose keys fit in shared memory (192 KB)
 
 struct Kv4SelectArgs {
@@ -46,9 +49,9 @@ __device__ __forceinline__ uint4 weight_keys(const float4& w, int i, int old) {
 template <bool CACHED>
 __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_constant__ Kv4SelectArgs a) {
   extern __shared__ uint4 cached[];
-  __shared__ int hist[EVICT_BINS];
+  __shared__ int hist[EVICT_COPIES][EVICT_BINS];
   __shared__ int warp_sum[32], warp_tie[32];
-  __shared__ int s_bin, s_need;
+  __shared__ int s_bin, s_need, s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = a.d.b * a.d.kv_heads;
   grid_dependents_start();
@@ -80,10 +83,10 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       const uint32_t digit = (1u << bits) - 1;
       __syncthreads();
-      for (int i = tid; i < EVICT_BINS; i += EVICT_THREADS) hist[i] = 0;
+      for (int i = tid; i < EVICT_COPIES * EVICT_BINS; i += EVICT_THREADS) (&hist[0][0])[i] = 0;
       __syncthreads();
       auto count = [&](uint32_t key) {
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1);
+        if ((key & mask) == prefix) atomicAdd(&hist[lane % EVICT_COPIES][(key >> shift) & digit], 1);
       };
 #pragma unroll 4
       for (int i = tid; i < quads; i += EVICT_THREADS) {
@@ -95,7 +98,12 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
       }
       __syncthreads();
       // from the top: thread i holds bins BINS - 1 - 2i and BINS - 2 - 2i
-      const int hi = hist[EVICT_BINS - 1 - 2 * tid], lo = hist[EVICT_BINS - 2 - 2 * tid];
+      int hi = 0, lo = 0;
+#pragma unroll
+      for (int x = 0; x < EVICT_COPIES; ++x) {
+        hi += hist[x][EVICT_BINS - 1 - 2 * tid];
+        lo += hist[x][EVICT_BINS - 2 - 2 * tid];
+      }
       int sum = hi + lo;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -104,17 +112,22 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
       }
       if (lane == 31) warp_sum[warp] = sum;
       __syncthreads();
-      int before = sum - hi - lo;
-      for (int i = 0; i < warp; ++i) before += warp_sum[i];
+      const int before = sum - hi - lo + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
       if (before < want && want <= before + hi + lo) {  // exactly one thread
         const bool in_hi = want <= before + hi;
         s_bin = EVICT_BINS - (in_hi ? 1 : 2) - 2 * tid;
         s_need = want - before - (in_hi ? 0 : hi);
+        s_count = in_hi ? hi : lo;
       }
       __syncthreads();
       prefix |= (uint32_t)s_bin << shift;
       mask |= digit << shift;
       want = s_need;
+      if (want == s_count && prefix != 0) {  // all that agree so far stay: they count as above
+        --prefix;
+        want = 0;
+        break;
+      }
     }
     // keys above `prefix` stay, and the first `want` of those equal to it;
     // each warp takes a run of whole 128s and first counts what stays before it
@@ -134,36 +147,47 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
       warp_tie[warp] = tie;
     }
     __syncthreads();
-    int above = 0, ties = 0;
-    for (int i = 0; i < warp; ++i) {
-      above += warp_sum[i];
-      ties += warp_tie[i];
-    }
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const int i = i0 + lane;
-      const uint4 k4 = i < hi ? keys_of(i, false) : make_uint4(0, 0, 0, 0);
-      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-      // counts above in the upper half, ties in the lower (at most 128 each)
-      int mine = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mine += k[e] > prefix ? 0x10000 : i < hi && k[e] == prefix ? 1 : 0;
-      int upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
+    int above = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
+    int ties = __reduce_add_sync(0xffffffffu, lane < warp ? warp_tie[lane] : 0);
+    const uint32_t below = (1u << lane) - 1;
+    if (want == 0) {  // no ties to choose from
+      for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        const uint4 k = i < hi ? keys_of(i, false) : make_uint4(0, 0, 0, 0);
+        const bool s0 = k.x > prefix, s1 = k.y > prefix, s2 = k.z > prefix, s3 = k.w > prefix;
+        const uint32_t b0 = __ballot_sync(0xffffffffu, s0), b1 = __ballot_sync(0xffffffffu, s1);
+        const uint32_t b2 = __ballot_sync(0xffffffffu, s2), b3 = __ballot_sync(0xffffffffu, s3);
+        int at = above + __popc(b0 & below) + __popc(b1 & below) + __popc(b2 & below) + __popc(b3 & below);
+        if (s0) kept[at++] = 4 * i;
+        if (s1) kept[at++] = 4 * i + 1;
+        if (s2) kept[at++] = 4 * i + 2;
+        if (s3) kept[at] = 4 * i + 3;
+        above += __popc(b0) + __popc(b1) + __popc(b2) + __popc(b3);
       }
-      const int all = __shfl_sync(0xffffffffu, upto, 31);
-      int at = above + ((upto - mine) >> 16), tied = ties + ((upto - mine) & 0xffff);
+    } else {
+      for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        const uint4 k4 = i < hi ? keys_of(i, false) : make_uint4(0, 0, 0, 0);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        int at = above, tied = ties;
+        bool is_above[4], is_tie[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool is_above = k[e] > prefix, is_tie = i < hi && k[e] == prefix;
-        if (is_above || (is_tie && tied < want)) kept[at + min(tied, want)] = 4 * i + e;
-        at += is_above;
-        tied += is_tie;
+        for (int e = 0; e < 4; ++e) {
+          is_above[e] = k[e] > prefix;
+          is_tie[e] = i < hi && k[e] == prefix;
+          const uint32_t b_above = __ballot_sync(0xffffffffu, is_above[e]), b_tie = __ballot_sync(0xffffffffu, is_tie[e]);
+          at += __popc(b_above & below);
+          tied += __popc(b_tie & below);
+          above += __popc(b_above);
+          ties += __popc(b_tie);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (is_above[e] || (is_tie[e] && tied < want)) kept[at + min(tied, want)] = 4 * i + e;
+          at += is_above[e];
+          tied += is_tie[e];
+        }
       }
-      above += all >> 16;
-      ties += all & 0xffff;
     }
     __syncthreads();
   }
