@@ -214,7 +214,11 @@ __device__ __forceinline__ int kva_token(int k) { return (k & 1) ? 7 - (k >> 1) 
 // groups of 16 tokens (its queries are zero in the products of the others), so
 // that one accumulator ends up with the scores of 16 F tokens and the softmax
 // costs a lane F times less; the copies' sums are added at the end of the run.
-template <int DH, int NT, int F>
+//
+// DIRECT: instead of the even split over the device, a block takes one segment,
+// splits it over its warps and joins their sums itself, which saves the second
+// kernel (kva_direct).
+template <int DH, int NT, int F, bool DIRECT>
 __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_kernel(const __grid_constant__ Kv4AttnArgs a) {
   static_assert(NT == 1 || F == 1, "copies of the queries fill one block of columns");
   using L = Kv4<DH>;
@@ -235,16 +239,23 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   __syncthreads();
   const Abort ab{flag, a.status};
 
-  uint32_t unused;
-  const KvaSplit split = kva_split(a, 0, unused);
-  const int rows = a.d.kv_heads * a.blocks_of_cols;
+  const int rows = a.d.kv_heads * a.blocks_of_cols, group = a.heads / a.d.kv_heads;
   if (blockIdx.x == 0 && warp == 0)
     for (int i = lane; i < a.d.b; i += 32) clamp_count(a.lens[i], a.d.capacity, a.status);
-  const int group = a.heads / a.d.kv_heads;
-  const int w = warp * gridDim.x + blockIdx.x;  // neighbours of a run on different SMs
-  if (w >= (int)split.warps || split.total == 0) return;
-  const uint32_t t0 = split.first(w);
-  KvaPlace at = kva_find(a, t0, (int)(split.first(w + 1) - t0), rows), next = at;
+  int w = 0;
+  KvaPlace at;
+  if constexpr (DIRECT) {
+    const int beta = blockIdx.x / rows, nb = kva_blocks(a, beta), each = nb / C::WARPS, rest = nb - each * C::WARPS;
+    at = KvaPlace{beta, (int)blockIdx.x - beta * rows, each * warp + min(warp, rest), nb, each + (warp < rest)};
+  } else {
+    uint32_t unused;
+    const KvaSplit split = kva_split(a, 0, unused);
+    w = warp * gridDim.x + blockIdx.x;  // neighbours of a run on different SMs
+    if (w >= (int)split.warps || split.total == 0) return;
+    const uint32_t t0 = split.first(w);
+    at = kva_find(a, t0, (int)(split.first(w + 1) - t0), rows);
+  }
+  KvaPlace next = at;
 
   int issued = 0;
   auto issue = [&]() {  // the next block of the run into its stage
@@ -270,7 +281,11 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   const uint32_t v_at[2] = {L::V_CODES + t * L::ROW + kv4_v_place<DH>(g, t) * 4u,
                             L::V_CODES + (7 - t) * L::ROW + kv4_v_place<DH>(g, 7 - t) * 4u};
   const int token = fold * 16 + kva_token(g);  // of this lane's results: 16 F j + token, and 8 on
+  // DIRECT: the warp's sums, in its ring once its blocks are done with
+  float* own_o = reinterpret_cast<float*>(smem_raw + (ring - smem_addr(smem_raw)));
+  float2* own_ml = reinterpret_cast<float2*>(own_o + 8 * NT * DH);
   int done = 0;
+  bool lost = false, summed = false;
   while (at.left > 0) {
     // one segment's part of the run
     const int len = min(max(a.lens[at.beta], 0), a.d.capacity);
@@ -502,7 +517,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
           while (!mbar_try_wait(bars + i % C::STAGES * 8, (i / C::STAGES) & 1) &&
                  global_timer_ns() - since < kWaitTimeoutNs) {}
         }
-        return;
+        lost = true;
+        break;
       }
       const int key0 = (at.blk + k) * KV4_BLOCK;
       if (key0 + KV4_BLOCK <= lim_all)
@@ -513,6 +529,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       ++done;
       issue();
     }
+
+    if (lost) break;
 
     // the run's sums for this segment: over the lanes of a column and its copies
     const long long slot = (long long)at.beta * rows + at.row + w;
@@ -534,7 +552,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         const int c = nt * 8 + 2 * t + e;
         const bool real = 2 * t < CW && col0 + c < a.cols;
         const long long to = slot * a.cols_block + c;
-        if (real && g == 0) a.part_ml[to] = make_float2(m[nt][e] * a.score_scale, sum);
+        if (real && g == 0) (DIRECT ? own_ml + c : a.part_ml + to)[0] = make_float2(m[nt][e] * a.score_scale, sum);
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
           const float add = fmaf(-135.5f, over_copies(ones[nt][gi][e]), over_lanes(off[nt][gi][e]));
@@ -545,13 +563,44 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             x[i + 4] = over_copies(o[nt][gi][i][e + 2]) + add;
           }
           if (real) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + to * DH + (gi * 8 + g) * 8);
+            float4* dst = reinterpret_cast<float4*>((DIRECT ? own_o + c * DH : a.part_o + to * DH) + (gi * 8 + g) * 8);
             dst[0] = make_float4(x[0], x[1], x[2], x[3]);
             dst[1] = make_float4(x[4], x[5], x[6], x[7]);
           }
         }
       }
+    summed = true;
     at.advance(a, rows, piece);
+  }
+
+  if constexpr (DIRECT) {
+    if (!summed && lane < 8 * NT) own_ml[lane] = make_float2(-INFINITY, 0.f);
+    __syncthreads();
+    const int beta = blockIdx.x / rows, row = blockIdx.x - beta * rows;
+    const int kvh = row / a.blocks_of_cols, col0 = (row - kvh * a.blocks_of_cols) * 8 * NT;
+    const int cols = min(a.cols - col0, 8 * NT);
+    const float* o0 = reinterpret_cast<const float*>(smem_raw + (smem - smem_addr(smem_raw)));
+    constexpr int STRIDE = C::STAGES * L::BYTES / 4;  // from warp to warp
+    for (int i = threadIdx.x; i < cols * DH; i += C::WARPS * 32) {
+      const int c = i / DH;
+      float m = -INFINITY, sum = 0.f, x = 0.f;
+#pragma unroll
+      for (int v = 0; v < C::WARPS; ++v) m = fmaxf(m, reinterpret_cast<const float2*>(o0 + v * STRIDE + 8 * NT * DH)[c].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int v = 0; v < C::WARPS; ++v) {
+        const float2 ml = reinterpret_cast<const float2*>(o0 + v * STRIDE + 8 * NT * DH)[c];
+        const float k = ex2_approx(ml.x - ref);
+        sum = fmaf(ml.y, k, sum);
+        // a warp without blocks has left nothing here (one whose blocks are all
+        // masked has left zeros)
+        if (ml.x != -INFINITY || ml.y != 0.f) x = fmaf(o0[v * STRIDE + i], k, x);
+      }
+      const bool none = sum == 0.f;  // a row that sees no token is zero
+      const int tok = (col0 + c) / group, head = kvh * group + col0 + c - tok * group;
+      a.o[(((long long)beta * a.n + tok) * a.heads + head) * DH + i - c * DH] = __float2bfloat16_rn(none ? 0.f : x / sum);
+      if (i == c * DH) a.lse2[((long long)beta * a.heads + head) * a.n + tok] = none ? -INFINITY : ref + log2f(sum);
+    }
   }
 }
 
@@ -560,26 +609,41 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 inline int kva_col_blocks(int cols) { return cols <= 8 ? 1 : 2; }
 
 typedef void (*KvaKernel)(const Kv4AttnArgs);
-template <int DH>
+template <int DH, bool DIRECT>
 KvaKernel kva_kernel(int cols) {
-  if (cols <= 2) return kv4_attention_kernel<DH, 1, 4>;
-  if (cols <= 4) return kv4_attention_kernel<DH, 1, 2>;
-  return cols <= 8 ? kv4_attention_kernel<DH, 1, 1> : kv4_attention_kernel<DH, 2, 1>;
+  if (cols <= 2) return kv4_attention_kernel<DH, 1, 4, DIRECT>;
+  if (cols <= 4) return kv4_attention_kernel<DH, 1, 2, DIRECT>;
+  return cols <= 8 ? kv4_attention_kernel<DH, 1, 1, DIRECT> : kv4_attention_kernel<DH, 2, 1, DIRECT>;
 }
 
-template <int DH>
-int kva_smem(int cols) {
-  return cols <= 8 ? KvaCfg<DH, 1>::SMEM : KvaCfg<DH, 2>::SMEM;
+inline KvaKernel kva_kernel(int dh, int cols, bool direct) {
+  if (dh == 128) return direct ? kva_kernel<128, true>(cols) : kva_kernel<128, false>(cols);
+  return direct ? kva_kernel<64, true>(cols) : kva_kernel<64, false>(cols);
+}
+
+inline int kva_smem(int dh, int cols) {
+  if (dh == 128) return cols <= 8 ? KvaCfg<128, 1>::SMEM : KvaCfg<128, 2>::SMEM;
+  return cols <= 8 ? KvaCfg<64, 1>::SMEM : KvaCfg<64, 2>::SMEM;
+}
+
+// Whether every segment gets a thread block of its own (DIRECT). It saves the
+// join, about 3.5 us, and costs the SMs that have no segment: a warp then has
+// `blocks` / `warps` blocks of tokens instead of that times segments / SMs, at
+// about 2 us a block. Device time of one call, direct against split: 4 segments
+// of 200 tokens (dh = 64) 4.6 against 8.2 us; 32 segments (dh = 128) of 1000
+// tokens 8.8 against 10.0, of 2000 tokens 12.1 against 10.1; 128 segments of 3000
+// tokens 15.4 against 18.1.
+inline bool kva_direct(long long segments, int blocks, int warps) {
+  return segments <= KVA_MAX_SMS && (long long)blocks * (KVA_MAX_SMS - segments) * 10 <= 16LL * warps * KVA_MAX_SMS;
 }
 
 inline bool kva_set_attributes() {
   bool ok = true;
-  for (int cols : {2, 4, 8, 16}) {
-    ok = ok && cudaFuncSetAttribute(kva_kernel<64>(cols), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kva_smem<64>(cols)) == cudaSuccess;
-    ok = ok && cudaFuncSetAttribute(kva_kernel<128>(cols), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kva_smem<128>(cols)) == cudaSuccess;
-  }
+  for (int dh : {64, 128})
+    for (int cols : {2, 4, 8, 16})
+      for (bool direct : {false, true})
+        ok = ok && cudaFuncSetAttribute(kva_kernel(dh, cols, direct), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kva_smem(dh, cols)) == cudaSuccess;
   return ok;
 }
 

@@ -402,16 +402,15 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   a.blocks_of_cols = L.passes;
   const int warps = kva_warps(dh, kva_col_blocks(L.cols)), most = std::min(sms, KVA_MAX_SMS);
   a.max_warps = std::min(L.max_warps, most * warps);
+  const long long segments = (long long)b * kv_heads * L.passes;
+  const bool direct = kva_direct(segments, capacity / KV4_BLOCK, warps);
   BPT_TRY(stream_status_word(st, &a.status));
   {
     LaunchScope ls("kv4_attention", st);
-    const unsigned grid = (unsigned)std::min(most, (a.max_warps + warps - 1) / warps);
-    if (dh == 128)
-      kva_kernel<128>(L.cols)<<<grid, warps * 32, kva_smem<128>(L.cols), st>>>(a);
-    else
-      kva_kernel<64>(L.cols)<<<grid, warps * 32, kva_smem<64>(L.cols), st>>>(a);
+    const unsigned grid = direct ? (unsigned)segments : (unsigned)std::min(most, (a.max_warps + warps - 1) / warps);
+    kva_kernel(dh, L.cols, direct)<<<grid, warps * 32, kva_smem(dh, L.cols), st>>>(a);
   }
-  {
+  if (!direct) {
     LaunchScope ls("kv4_join", st);
     const dim3 grid((unsigned)(kv_heads * L.cols), grid_y(b));
     BPT_TRY(launch_dependent(dh == 128 ? kv4_join_kernel<128> : kv4_join_kernel<64>, a, grid, KVJ_WARPS * 32, st));

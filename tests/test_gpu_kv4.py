@@ -200,11 +200,14 @@ def check_attention(q, cache, held, lens, heads, causal=True, weights=None, **kw
 @pytest.mark.parametrize("dh", [64, 128])
 @pytest.mark.parametrize("heads,kv,n", [(1, 1, 1), (4, 4, 1), (8, 1, 1), (6, 2, 1), (5, 5, 3), (20, 4, 2), (2, 2, 17),
                                         (40, 1, 1), (9, 3, 12)])
-def test_attention_over_odd_lengths(heads, kv, n, dh):
+@pytest.mark.parametrize("capacity", [256, 20032])
+def test_attention_over_odd_lengths(heads, kv, n, dh, capacity):
+    # in a short cache a thread block takes a head; in a long one the blocks of
+    # all heads are split over the device
     lens = [1, 64, 0, 65, 200, 63, 127]
-    cache, held = filled(len(lens), kv, dh, lens, 256, seed=heads)
+    cache, held = filled(len(lens), kv, dh, lens, capacity, seed=heads)
     q = bf16((len(lens), n, heads * dh), 7)
-    w = torch.rand((len(lens), kv, 256), generator=torch.Generator().manual_seed(0)).cuda()
+    w = torch.rand((len(lens), kv, capacity), generator=torch.Generator().manual_seed(0)).cuda()
     check_attention(q, cache, held, lens, heads)
     check_attention(q, cache, held, lens, heads, weights=w)
     check_attention(q, cache, held, lens, heads, causal=False, weights=w)
