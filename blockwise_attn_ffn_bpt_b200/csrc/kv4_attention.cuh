@@ -13,14 +13,17 @@
 // tokens) are the 8 columns of m16n8k16 products, 16 cached tokens (K) or 16
 // dimensions (V) their rows:
 //     S^T[16 tokens, 8] = K[16, dh] Q^T,   O^T[dh, 8] += V^T[dh, 16] P^T.
-// A K nibble with one logical operation is the bf16 number 16 + code, a V
-// nibble 128 + code; scale and minimum enter after the product with K and
-// before the one with V:
+// A nibble, shifted into bits 3 .. 6 of a 16-bit half, with one logical
+// operation is the bf16 number 16 + code; scale and minimum enter after the
+// product with K and before the one with V:
 //     s   = sum over groups of scale (q . (16 + code) - 16 sum q) + min sum q
-//     o   = sum_u P' (128 + code) - 135.5 sum_u P' + sum_u p mid,
+//     o   = sum_u P' (16 + code) - 23.5 sum_u P' + sum_u p mid,
 // P' = bf16(p scale), mid = min + 7.5 scale: P' rounds what multiplies code -
-// 7.5, not code, and the sum of P' is one more product (with ones), so the
-// offset cancels to fp32 accuracy.
+// 7.5, not code. The sum of P' is one more product (with ones); it is taken off
+// after every block of tokens, since the offset would otherwise grow along the
+// run until the roundings of its sum drown the values' (at 32768 tokens of equal
+// weight, whose mean is small, o was 1.6e-2 off in the norm with an offset of 128
+// taken off at the end, of which 2.0e-3 is the rounding of P' and o to bf16).
 //
 // The cached blocks of all sequences and heads, one after the other, are split
 // evenly over the warps of the device, whatever the lengths. A warp works on
@@ -273,8 +276,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   const int fold = 2 * t / CW;           // the copy that this lane's two columns of a result belong to
   const int row_fold = F == 1 ? 0 : g / CW;  // the copy that this lane's column of an operand belongs to
   const float lazy = KVA_LAZY / a.score_scale;
-  // the masks of and_or, which are most of what the arithmetic units do here
-  const uint32_t k_mask = 0x00780078u + a.zero, v_mask = 0x000f000fu + a.zero;
+  const uint32_t mask = 0x00780078u + a.zero;  // of and_or, which is most of what the arithmetic units do here
   // where this lane's words and parameters lie in a block, the compile-time
   // parts left out (8 rows on, V's words lie in the same order)
   const uint32_t k_at = kva_token(g) * L::ROW + t * (L::ROW / 4);
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 
     // m: the maximum's reference, in units of a score before score_scale; the
     // sums of a lane are of its own tokens until the end of the run
-    float o[NT][G][4][4] = {}, ones[NT][G][4] = {};
+    float o[NT][G][4][4] = {};
     float m[NT][2], ref[NT][2] = {}, l[NT][2] = {}, off[NT][G][2] = {};  // ref: m score_scale, or 0 for none
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
@@ -362,8 +364,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             uint32_t xa[4], xb[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              xa[e] = and_or<0x41804180u>(__funnelshift_r(ka[i], ka[i], 4 * e), k_mask);
-              xb[e] = and_or<0x41804180u>(__funnelshift_r(kb[i], kb[i], 4 * e), k_mask);
+              xa[e] = and_or<0x41804180u>(__funnelshift_r(ka[i], ka[i], 4 * e), mask);
+              xb[e] = and_or<0x41804180u>(__funnelshift_r(kb[i], kb[i], 4 * e), mask);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -392,6 +394,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             s[j][nt][e] = x;
           }
       }
+      float ones[NT][G][4];  // sums of P' over the block
       if (a.scores != nullptr) {
         float* to = a.scores + ((long long)at.beta * a.d.kv_heads + kvh) * a.cols * a.d.capacity + key0 + token;
 #pragma unroll
@@ -435,7 +438,6 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) {
               off[nt][gi][e] *= f;
-              ones[nt][gi][e] *= f;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 o[nt][gi][i][e] *= f;
@@ -475,8 +477,9 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             }
             bf[nt][gi][0] = transpose8(pack_bf16x2(x[0], x[1]));
             bf[nt][gi][1] = transpose8(pack_bf16x2(x[2], x[3]));
+            float none[4] = {};
             mma16816(ones[nt][gi], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, bf[nt][gi][0], bf[nt][gi][1],
-                     ones[nt][gi]);
+                     j == 0 ? none : ones[nt][gi]);
           }
         }
 #pragma unroll
@@ -497,14 +500,22 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
               for (int x = 0; x < 2; ++x) b[nt][x] = F == 1 || row_fold == f ? bf[nt][gi][x] : 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t a0 = and_or<0x43004300u>(lo0 >> (4 * i), v_mask), a1 = and_or<0x43004300u>(hi0 >> (4 * i), v_mask);
-              const uint32_t a2 = and_or<0x43004300u>(lo1 >> (4 * i), v_mask), a3 = and_or<0x43004300u>(hi1 >> (4 * i), v_mask);
+              auto code = [&](uint32_t x) { return and_or<0x41804180u>(i == 0 ? x << 3 : x >> (4 * i - 3), mask); };
+              const uint32_t a0 = code(lo0), a1 = code(hi0), a2 = code(lo1), a3 = code(hi1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][gi][i], a0, a1, a2, a3, b[nt][0], b[nt][1], o[nt][gi][i]);
             }
           }
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][gi][i][e] = fmaf(-23.5f, ones[nt][gi][e & 1], o[nt][gi][i][e]);
     };
 
     const int piece = min(at.nb - at.blk, at.left);
@@ -555,7 +566,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         if (real && g == 0) (DIRECT ? own_ml + c : a.part_ml + to)[0] = make_float2(m[nt][e] * a.score_scale, sum);
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
-          const float add = fmaf(-135.5f, over_copies(ones[nt][gi][e]), over_lanes(off[nt][gi][e]));
+          const float add = over_lanes(off[nt][gi][e]);
           float x[8];  // dimensions 8u .. 8u + 7 of word u = 8 gi + g
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

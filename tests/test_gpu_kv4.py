@@ -239,6 +239,25 @@ def test_attention_with_large_and_equal_scores():
         assert (np.abs(heads_of(o, 2)[0, 0, 1] - mean) <= 2.0 ** -8 * (np.abs(mean) + 7.5 * held[0]["vs"].max())).all()
 
 
+@pytest.mark.parametrize("dh", [64, 128])
+def test_the_mean_of_a_long_cache_keeps_its_accuracy(dh):
+    # Zero queries: every weight is the same and P' is V's scale, without a
+    # rounding; o is V's mean. 128 heads of 131072 tokens, the same 64 over and
+    # over, are long runs for every warp. What is left beside o's rounding are
+    # the fp32 sums of at most 31 scale a token: 2^-20 of that.
+    b, kv, blocks = 4, 32, 2048
+    small, held = filled(b, kv, dh, [64] * b, 64, seed=21)
+    cache = bpt.KV4Cache(small.data.repeat(1, 1, blocks, 1), dh)
+    q = torch.zeros((b, 1, kv * dh), dtype=torch.bfloat16, device="cuda")
+    n = 64 * blocks
+    o, lse2 = bpt.kv4_attention(q, cache, ints(*[n] * b), kv, return_lse=True)
+    assert ((lse2 - np.log2(n)).abs() <= 2.0 ** -20 + 2.0 ** -19).all()
+    got = heads_of(o, kv)[:, 0]
+    mean = np.stack([x["v"].mean(1) for x in held])
+    step = np.stack([x["vs"].max() for x in held])[:, None, None]
+    assert (np.abs(got - mean) <= 2.0 ** -8 * np.abs(mean) + 2.0 ** -20 * 31 * step).all()
+
+
 def test_what_lies_past_the_length_does_not_matter_and_nan_inside_shows():
     cache, held = filled(2, 2, 128, [100, 30], 192, seed=13)
     q = bf16((2, 1, 4 * 128), 14)
