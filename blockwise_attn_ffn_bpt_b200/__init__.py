@@ -475,7 +475,8 @@ def _rows(t: torch.Tensor, name: str, width: int, dtypes, like: Optional[torch.T
         raise TypeError(f"{name} has dtype {dtype}")
     if len(shape) != 3 or shape[2] != width:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected [b, s, {width}]")
-    if like is not None and (shape[:2] != like.shape[:2] or dtype != like.dtype or t.get_device() != like.get_device()):
+    if like is not None and (shape[0] != like.shape[0] or shape[1] != like.shape[1] or dtype != like.dtype
+                             or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have the tokens, dtype and device of the first tensor")
     if stride[2] != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
@@ -484,7 +485,7 @@ def _rows(t: torch.Tensor, name: str, width: int, dtypes, like: Optional[torch.T
 
 def _new_rows(like: torch.Tensor, b: int, s: int, width: int) -> tuple:
     """A new contiguous tensor [b, s, width], the shape of `like`, and its place as of _rows."""
-    t = torch.empty_like(like) if like.is_contiguous() else like.new_empty((b, s, width))
+    t = torch.empty_like(like) if like.is_contiguous() else torch.empty(b, s, width, dtype=like.dtype, device=like.device)
     return t, (t.data_ptr(), s * width, width)
 
 
@@ -525,10 +526,12 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], heads: int, kv_heads: int
     positions: int32 or int64, [b, s] or [s], or None: token t is at offset +
     t. inverse=True is the gradient: dq, dk of the turned q, k in, of q, k out.
     q_out and k_out may be q and k themselves. Returns (q_out, k_out)."""
-    b, s = q.shape[:2]
-    if heads <= 0 or q.shape[-1] % heads:
-        raise ValueError(f"q's last dimension {q.shape[-1]} does not hold {heads} heads")
-    dh = q.shape[-1] // heads
+    if q.dim() != 3:
+        raise ValueError("q must be [b, s, heads * dh]")
+    b, s, width = q.shape
+    if heads <= 0 or width % heads:
+        raise ValueError(f"q's last dimension {width} does not hold {heads} heads")
+    dh = width // heads
     kinds = (torch.bfloat16, torch.float32)
     pq = _rows(q, "q", heads * dh, kinds)
     if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
@@ -640,7 +643,7 @@ def kv4_load(cache: KV4Cache, lens: torch.Tensor, n: int, start: Optional[torch.
     ps = None if start is None else cache._ints(start, "start")
     dev = cache.data.device
     with _On(dev.index, stream) as st:
-        k = cache.data.new_empty((cache.b, n, cache.kv_heads * cache.dh), dtype=torch.bfloat16)
+        k = torch.empty(cache.b, n, cache.kv_heads * cache.dh, dtype=torch.bfloat16, device=dev)
         v = torch.empty_like(k)
         r = lib().bpt_kv4_load(*cache._args(), ps, pl, n, k.data_ptr(), v.data_ptr(), st)
     _check(r, "bpt_kv4_load")
@@ -670,11 +673,11 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, heads: i
     nbytes = _kv4_workspace_bytes(b, n, heads, kv_heads, capacity, dh, pw is not None)
     with _On(dev.index, stream) as st:
         o = _new_rows(q, b, n, heads * dh)[0]
-        lse2 = q.new_empty((b, heads, n), dtype=torch.float32) if return_lse else None
-        ws = cache.data.new_empty(max(nbytes, 1))
+        lse2 = torch.empty(b, heads, n, dtype=torch.float32, device=dev) if return_lse else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         r = lib().bpt_kv4_attention(*pq, data, pl, b, n, heads, kv_heads, capacity, dh, int(bool(causal)),
-                                    o.data_ptr(), None if lse2 is None else lse2.data_ptr(), pw, ws.data_ptr(),
-                                    ws.numel(), st)
+                                    o.data_ptr(), None if lse2 is None else lse2.data_ptr(), pw,
+                                    ws.data_ptr() if nbytes else None, nbytes, st)
     _check(r, "bpt_kv4_attention")
     return (o, lse2) if return_lse else o
 
@@ -691,9 +694,9 @@ def kv4_evict(cache: KV4Cache, weights: torch.Tensor, lens: torch.Tensor, keep: 
     pw, pl = cache._floats(weights, "weights"), cache._ints(lens, "lens")
     data, b, kv_heads, capacity, dh = cache._args()
     with _On(dev.index, stream) as st:
-        kept = lens.new_empty((b, kv_heads, max(int(keep), 0)))
-        new_lens = lens.new_empty(b)
-        new_weights = weights.new_empty((b, kv_heads, out.capacity))
+        kept = torch.empty(b, kv_heads, max(int(keep), 0), dtype=torch.int32, device=dev)
+        new_lens = torch.empty_like(lens)
+        new_weights = torch.empty(b, kv_heads, out.capacity, dtype=torch.float32, device=dev)
         r = lib().bpt_kv4_evict(data, pw, pl, b, kv_heads, capacity, dh, int(keep), int(recent), out.data.data_ptr(),
                                 out.capacity, new_weights.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), st)
     _check(r, "bpt_kv4_evict")

@@ -72,7 +72,7 @@ struct Kv4AttnArgs {
   uint32_t zero;
   float score_scale;       // log2(e) / sqrt(dh)
   __nv_bfloat16* o;        // [b, n, heads * dh]
-  float* lse2;             // [b, heads, n]
+  float* lse2;             // [b, heads, n], or null
   float* scores;           // [b, kv_heads, cols, capacity] in log2 units, or null
   float* part_o;           // [slots][cols_block][dh]: sums of a run, not divided
   float2* part_ml;         // [slots][cols_block]: maximum and sum
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       const bool none = sum == 0.f;  // a row that sees no token is zero
       const int tok = (col0 + c) / group, head = kvh * group + col0 + c - tok * group;
       a.o[(((long long)beta * a.n + tok) * a.heads + head) * DH + i - c * DH] = __float2bfloat16_rn(none ? 0.f : x / sum);
-      if (i == c * DH) a.lse2[((long long)beta * a.heads + head) * a.n + tok] = none ? -INFINITY : ref + log2f(sum);
+      if (i == c * DH && a.lse2 != nullptr) a.lse2[((long long)beta * a.heads + head) * a.n + tok] = none ? -INFINITY : ref + log2f(sum);
     }
   }
 }
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_c
       for (int i = 0; i < KVJ_WARPS; ++i) x = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - ref), x);
       a.o[(((long long)beta * a.n + tok) * a.heads + head) * DH + threadIdx.x] = __float2bfloat16_rn(none ? 0.f : x / sum);
     }
-    if (threadIdx.x == 0) a.lse2[((long long)beta * a.heads + head) * a.n + tok] = none ? -INFINITY : ref + log2f(sum);
+    if (threadIdx.x == 0 && a.lse2 != nullptr) a.lse2[((long long)beta * a.heads + head) * a.n + tok] = none ? -INFINITY : ref + log2f(sum);
     __syncthreads();
   }
 }

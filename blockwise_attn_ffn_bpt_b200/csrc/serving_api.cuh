@@ -113,7 +113,9 @@ void launch_rotary(const RotaryArgs& a, bool interleaved, dim3 grid, cudaStream_
 
 struct Kv4AttnLayout {
   size_t lse = 0, ml = 0, o = 0, scores = 0, total = 0;
-  int cols = 0, cols_block = 0, passes = 0, max_warps = 0;
+  int cols = 0, cols_block = 0, passes = 0, warps = 0, max_warps = 0;
+  long long segments = 0;
+  bool direct = false;
 };
 
 Kv4AttnLayout kv4_attn_layout(int b, int n, int heads, int kv_heads, int capacity, int dh, bool weights) {
@@ -122,19 +124,24 @@ Kv4AttnLayout kv4_attn_layout(int b, int n, int heads, int kv_heads, int capacit
   const int pass = 8 * kva_col_blocks(l.cols);  // more queries take further passes over the head's tokens
   l.cols_block = std::min(l.cols, pass);
   l.passes = (l.cols + pass - 1) / pass;
-  const size_t segments = (size_t)b * kv_heads * l.passes;
-  const int warps = kva_warps(dh, pass / 8);
-  l.max_warps = (int)std::min<size_t>(segments * (capacity / KV4_BLOCK), (size_t)KVA_MAX_SMS * warps);
-  const size_t slots = segments + l.max_warps;
+  l.segments = (long long)b * kv_heads * l.passes;
+  l.warps = kva_warps(dh, pass / 8);
+  l.direct = kva_direct(l.segments, capacity / KV4_BLOCK, l.warps);
+  l.max_warps = (int)std::min<long long>(l.segments * (capacity / KV4_BLOCK), (long long)KVA_MAX_SMS * l.warps);
   size_t at = 0;
   auto take = [&](size_t& to, size_t bytes) {
     to = at;
     at += align_up(bytes, 256);
   };
-  take(l.lse, (size_t)b * heads * n * 4);
-  take(l.ml, slots * l.cols_block * 8);
-  take(l.o, slots * l.cols_block * dh * 4);
-  if (weights) take(l.scores, (size_t)b * heads * n * capacity * 4);
+  if (!l.direct) {
+    const size_t slots = (size_t)l.segments + l.max_warps;
+    take(l.ml, slots * l.cols_block * 8);
+    take(l.o, slots * l.cols_block * dh * 4);
+  }
+  if (weights) {
+    take(l.lse, (size_t)b * heads * n * 4);
+    take(l.scores, (size_t)b * heads * n * capacity * 4);
+  }
   l.total = at;
   return l;
 }
@@ -359,13 +366,13 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
                       float* weights, void* workspace, size_t ws_bytes, void* stream) {
   BPT_TRY(check_kv4_attention(b, n, heads, kv_heads, capacity, dh));
   if (b == 0 || n == 0) return BPT_OK;
-  if (!q || !cache || !lens || !o || !workspace) return BPT_ERR_NULL;
+  const Kv4AttnLayout L = kv4_attn_layout(b, n, heads, kv_heads, capacity, dh, weights != nullptr);
+  if (!q || !cache || !lens || !o || (!workspace && L.total)) return BPT_ERR_NULL;
   const TokenRows rq{q, b, n, bs_q * 2, ld_q * 2, (size_t)heads * dh * 2};
   if (!strides_ok(rq)) return BPT_ERR_SHAPE;
   if (!aligned16(cache) || !aligned(rq, 16) || !aligned16(o) || !aligned16(lse2) || !aligned16(weights))
     return BPT_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(lens) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return BPT_ERR_ALIGN;
-  const Kv4AttnLayout L = kv4_attn_layout(b, n, heads, kv_heads, capacity, dh, weights != nullptr);
   if (ws_bytes < L.total) return BPT_ERR_NOMEM;
   const size_t rows = (size_t)b * n * heads;
   const Range in[3] = {rq.range(), rng(cache, kv4_bytes(b, kv_heads, capacity, dh)), rng(lens, (size_t)b * 4)};
@@ -393,24 +400,22 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   a.causal = causal != 0;
   a.score_scale = (float)(1.4426950408889634 / std::sqrt((double)dh));
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
-  a.lse2 = lse2 ? lse2 : reinterpret_cast<float*>(ws + L.lse);
+  a.lse2 = lse2 || !weights ? lse2 : reinterpret_cast<float*>(ws + L.lse);
   a.scores = weights ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
   a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
   a.part_o = reinterpret_cast<float*>(ws + L.o);
   a.cols = L.cols;
   a.cols_block = L.cols_block;
   a.blocks_of_cols = L.passes;
-  const int warps = kva_warps(dh, kva_col_blocks(L.cols)), most = std::min(sms, KVA_MAX_SMS);
-  a.max_warps = std::min(L.max_warps, most * warps);
-  const long long segments = (long long)b * kv_heads * L.passes;
-  const bool direct = kva_direct(segments, capacity / KV4_BLOCK, warps);
+  const int most = std::min(sms, KVA_MAX_SMS);
+  a.max_warps = std::min(L.max_warps, most * L.warps);
   BPT_TRY(stream_status_word(st, &a.status));
   {
     LaunchScope ls("kv4_attention", st);
-    const unsigned grid = direct ? (unsigned)segments : (unsigned)std::min(most, (a.max_warps + warps - 1) / warps);
-    kva_kernel(dh, L.cols, direct)<<<grid, warps * 32, kva_smem(dh, L.cols), st>>>(a);
+    const unsigned grid = L.direct ? (unsigned)L.segments : (unsigned)std::min(most, (a.max_warps + L.warps - 1) / L.warps);
+    kva_kernel(dh, L.cols, L.direct)<<<grid, L.warps * 32, kva_smem(dh, L.cols), st>>>(a);
   }
-  if (!direct) {
+  if (!L.direct) {
     LaunchScope ls("kv4_join", st);
     const dim3 grid((unsigned)(kv_heads * L.cols), grid_y(b));
     BPT_TRY(launch_dependent(dh == 128 ? kv4_join_kernel<128> : kv4_join_kernel<64>, a, grid, KVJ_WARPS * 32, st));

@@ -541,7 +541,9 @@ int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, c
  * kv_heads, capacity], or NULL: every place's softmax weight, summed over the
  * new tokens and the heads that share it, is ADDED to it (places at or past
  * lens[beta] are left as they are). The scores and all sums are fp32; the
- * softmax weights enter the product with V as bf16, times the scale of V. */
+ * softmax weights enter the product with V as bf16, times the scale of V.
+ * workspace: bpt_kv4_attention_workspace_bytes of the same arguments, which may
+ * be 0 (short caches without weights; workspace may then be NULL). */
 size_t bpt_kv4_attention_workspace_bytes(int b, int n, int heads, int kv_heads, int capacity, int dh,
                                          int with_weights);
 int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void* cache, const int* lens, int b,
