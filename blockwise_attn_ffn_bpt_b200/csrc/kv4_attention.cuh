@@ -35,14 +35,11 @@
 #include <type_traits>
 
 #include "kv4_cache.cuh"
+#include "kv4_split.h"
 
 namespace bpt {
 
 constexpr int KVA_MAX_SMS = 148;      // the split does not grow past it (workspaces are sized without a device)
-// Blocks that the start of a segment takes as long as (KvaSplit). Measured at 16
-// contexts of 4096 tokens, 32 heads of 128: 62.1 us with 0, 61.3 with 1, 61.9
-// with 2; at 8 of 32768 tokens 200.7, 198.8 and 199.9.
-constexpr int KVA_SWITCH = 1;
 constexpr float KVA_LAZY = 8.0f;      // the maximum is raised when a score passes it by this (log2)
 
 // Warps of an SM and stages of a warp: the rings take 216 KB in every case, and
@@ -84,28 +81,6 @@ __device__ __forceinline__ int kv4_seen(int len, int n, int t, int causal) {
   return causal ? max(len - n + 1 + t, 0) : len;
 }
 
-// The even split. Segments are (sequence, head, block of columns) in that
-// order. A segment of nb > 0 blocks of 64 tokens counts nb + KVA_SWITCH units:
-// the first ones stand for the start of a segment (its queries, and the sums of
-// the one before), which takes a warp about as long as that many blocks. The
-// `total` units of all segments (below 2^31) are cut into one run a warp; the
-// first total % warps ones have one unit more than the others. The result of
-// warp w for segment s goes to slot s + w (both grow along the run, so no two
-// share one).
-struct KvaSplit {
-  uint32_t total, warps, each, rest;
-  __device__ __forceinline__ KvaSplit(uint32_t t, uint32_t max_warps) : total(t) {
-    warps = max(1u, min(t, max_warps));
-    each = t / warps;
-    rest = t - each * warps;
-  }
-  __device__ __forceinline__ uint32_t first(uint32_t w) const { return each * w + min(w, rest); }
-  __device__ __forceinline__ uint32_t warp_of(uint32_t block) const {
-    const uint32_t longer = (each + 1) * rest;
-    return block < longer ? block / (each + 1) : rest + (block - longer) / each;
-  }
-};
-
 __device__ __forceinline__ int kva_blocks(const Kv4AttnArgs& a, int beta) {
   return (min(max(a.lens[beta], 0), a.d.capacity) + KV4_BLOCK - 1) / KV4_BLOCK;
 }
@@ -116,7 +91,7 @@ __device__ __forceinline__ KvaSplit kva_split(const Kv4AttnArgs& a, int beta, ui
   uint32_t total = 0, prior = 0;
   for (int i = lane_id(); i < a.d.b; i += 32) {
     const uint32_t nb = kva_blocks(a, i);
-    const uint32_t units = nb ? nb + KVA_SWITCH : 0;
+    const uint32_t units = kva_units(nb);
     total += units;
     if (i < beta) prior += units;
   }
@@ -124,33 +99,13 @@ __device__ __forceinline__ KvaSplit kva_split(const Kv4AttnArgs& a, int beta, ui
   return KvaSplit(__reduce_add_sync(0xffffffffu, total) * per, (uint32_t)a.max_warps);
 }
 
-// A place in a run: block `blk` of row `row` (head and block of columns) of
-// sequence beta, which has nb blocks; `left` units of the run from there on.
-struct KvaPlace {
-  int beta, row, blk, nb, left;
-  // Takes n blocks; at the end of a segment, on to the next one.
-  __device__ __forceinline__ void advance(const Kv4AttnArgs& a, int rows, int n) {
-    blk += n;
-    left -= n;
-    if (blk < nb || left <= 0) return;
-    blk = 0;
-    if (++row == rows) {
-      row = 0;
-      do ++beta;
-      while (beta < a.d.b && (nb = kva_blocks(a, beta)) == 0);
-      if (beta == a.d.b) left = 0;
-    }
-    left -= KVA_SWITCH;
-  }
-};
-
 // The place of unit t, and the run of n units from there (whole warp).
 __device__ __forceinline__ KvaPlace kva_find(const Kv4AttnArgs& a, uint32_t t, int n, int rows) {
   uint32_t base = 0;
   const int lane = lane_id();
   for (int b0 = 0; b0 < a.d.b; b0 += 32) {
     const uint32_t nb = b0 + lane < a.d.b ? kva_blocks(a, b0 + lane) : 0;
-    const uint32_t units = nb ? (nb + KVA_SWITCH) * rows : 0;
+    const uint32_t units = kva_units(nb) * rows;
     uint32_t sum = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -161,9 +116,7 @@ __device__ __forceinline__ KvaPlace kva_find(const Kv4AttnArgs& a, uint32_t t, i
     if (past) {
       const int src = __ffs(past) - 1;
       const uint32_t blocks = __shfl_sync(0xffffffffu, nb, src);
-      const uint32_t r = t - (base + __shfl_sync(0xffffffffu, sum - units, src)), row = r / (blocks + KVA_SWITCH);
-      const int unit = r - row * (blocks + KVA_SWITCH), start = max(KVA_SWITCH - unit, 0);
-      return KvaPlace{b0 + src, (int)row, max(unit - KVA_SWITCH, 0), (int)blocks, n - start};
+      return KvaPlace::in_sequence(b0 + src, blocks, t - (base + __shfl_sync(0xffffffffu, sum - units, src)), n);
     }
     base += __shfl_sync(0xffffffffu, sum, 31);
   }
@@ -260,6 +213,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   }
   KvaPlace next = at;
 
+  auto blocks_of = [&](int beta) { return kva_blocks(a, beta); };
   int issued = 0;
   auto issue = [&]() {  // the next block of the run into its stage
     if (next.left <= 0) return;
@@ -271,7 +225,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       bulk_load(ring + issued % C::STAGES * L::BYTES, src, L::BYTES, bar);
     }
     ++issued;
-    next.advance(a, rows, 1);
+    next.advance(blocks_of, a.d.b, rows, 1);
   };
   const int fold = 2 * t / CW;           // the copy that this lane's two columns of a result belong to
   const int row_fold = F == 1 ? 0 : g / CW;  // the copy that this lane's column of an operand belongs to
@@ -581,7 +535,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         }
       }
     summed = true;
-    at.advance(a, rows, piece);
+    at.advance(blocks_of, a.d.b, rows, piece);
   }
 
   if constexpr (DIRECT) {
@@ -682,7 +636,7 @@ __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_c
     const int nb = kva_blocks(a, beta), row = kvh * a.blocks_of_cols + cb;
     int w0 = 0, w1 = -1;
     if (nb > 0) {
-      const uint32_t first = before + (uint32_t)row * (nb + KVA_SWITCH) + KVA_SWITCH;
+      const uint32_t first = before + kva_first_block(row, nb);
       w0 = split.warp_of(first);
       w1 = split.warp_of(first + nb - 1);
     }
