@@ -13,17 +13,27 @@
 // tokens) are the 8 columns of m16n8k16 products, 16 cached tokens (K) or 16
 // dimensions (V) their rows:
 //     S^T[16 tokens, 8] = K[16, dh] Q^T,   O^T[dh, 8] += V^T[dh, 16] P^T.
-// A nibble, shifted into bits 3 .. 6 of a 16-bit half, with one logical
-// operation is the bf16 number 16 + code; scale and minimum enter after the
-// product with K and before the one with V:
-//     s   = sum over groups of scale (q . (16 + code) - 16 sum q) + min sum q
-//     o   = sum_u P' (16 + code) - 23.5 sum_u P' + sum_u p mid,
-// P' = bf16(p scale), mid = min + 7.5 scale: P' rounds what multiplies code -
-// 7.5, not code. The sum of P' is one more product (with ones); it is taken off
-// after every block of tokens, since the offset would otherwise grow along the
-// run until the roundings of its sum drown the values' (at 32768 tokens of equal
-// weight, whose mean is small, o was 1.6e-2 off in the norm with an offset of 128
-// taken off at the end, of which 2.0e-3 is the rounding of P' and o to bf16).
+// A nibble that lies within the 10 lowest bits of a 16-bit half is, masked, a
+// subnormal fp16 number: code 2^e, exactly, with e from its place. So one
+// operation (and a shift for some) makes an operand of two codes, and nothing
+// has to be taken off the products; powers of two that differ by the place are
+// in the other operand (K) or taken out at the end (V). Scale and minimum enter
+// after the product with K and before the one with V, for groups of 64 dims:
+//     s = sum over groups of scale (q . code) + min (sum q),
+//     o = sum_u P' code + sum_u p min,   P' = p scale.
+// q enters as fp16 times a power of two that takes its largest element to 2^14
+// (exact but for elements 2^-25 below that). P' enters as fp16 times a factor w
+// of its column and group, w P' being at most 2^14 and 2^7 where w is set: what
+// lies 2^-31 below the largest P' so far is lost, everything above 2^-21 of it
+// keeps fp16's 11 bits. w falls when a P' would pass 2^14, and rises with the
+// softmax's maximum, which takes the P' of the tokens before with it.
+//
+// The sum of P' code, 7.5 times that of P' and more, would lose the values' small
+// mean over many tokens in its roundings. So every KVA_CENTRE blocks 7.5 sum P'
+// is taken off it, and the second sum is of p mid, mid = min + 7.5 scale. (At
+// 32768 tokens of equal weight o was 1.6e-2 off in the norm with an offset of
+// 135 P' a token in that sum until its end; the rounding of o to bf16 alone is
+// 1.7e-3.)
 //
 // The cached blocks of all sequences and heads, one after the other, are split
 // evenly over the warps of the device, whatever the lengths. A warp works on
@@ -31,6 +41,8 @@
 // and O^T; it leaves a partial result for each (sequence, head) that its run
 // touches, and kv4_join_kernel joins those.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include <type_traits>
 
@@ -40,6 +52,8 @@
 namespace bpt {
 
 constexpr int KVA_MAX_SMS = 148;      // the split does not grow past it (workspaces are sized without a device)
+constexpr int KVA_CENTRE = 16;
+constexpr float KVA_HIGH = 16384.0f, KVA_WIDEST = 0x1p100f;  // of w P' and of w
 constexpr float KVA_LAZY = 8.0f;      // the maximum is raised when a score passes it by this (log2)
 
 // Warps of an SM and stages of a warp: the rings take 216 KB in every case, and
@@ -66,7 +80,6 @@ struct Kv4AttnArgs {
   int n, heads, causal;
   int cols, cols_block, blocks_of_cols;  // queries that share a head; those of one pass over it; passes
   int max_warps;
-  uint32_t zero;
   float score_scale;       // log2(e) / sqrt(dh)
   __nv_bfloat16* o;        // [b, n, heads * dh]
   float* lse2;             // [b, heads, n], or null
@@ -129,17 +142,22 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// d = A B + c
+// d = A B + c, fp16 operands
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1, const float (&c)[4]) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// The transpose of an 8 x 8 matrix of bf16 held two to a lane.
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values held two to a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -230,7 +248,6 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   const int fold = 2 * t / CW;           // the copy that this lane's two columns of a result belong to
   const int row_fold = F == 1 ? 0 : g / CW;  // the copy that this lane's column of an operand belongs to
   const float lazy = KVA_LAZY / a.score_scale;
-  const uint32_t mask = 0x00780078u + a.zero;  // of and_or, which is most of what the arithmetic units do here
   // where this lane's words and parameters lie in a block, the compile-time
   // parts left out (8 rows on, V's words lie in the same order)
   const uint32_t k_at = kva_token(g) * L::ROW + t * (L::ROW / 4);
@@ -248,7 +265,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
     const int kvh = at.row / a.blocks_of_cols, cb = at.row - kvh * a.blocks_of_cols;
     const int col0 = cb * 8 * NT;
     uint32_t qf[NT][F][KW][4];
-    float qs[NT][G][2], init[NT][G][4];
+    float qs[NT][G][2], unit[NT][2];  // sums of q; what a product of q with codes is times q and codes
     int lim[NT][2];
     uint4 raw[NT][KW];
 #pragma unroll
@@ -265,29 +282,47 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       for (int i = 0; i < C::STAGES; ++i) issue();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      uint32_t top = 0;  // largest |q|, as bits
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const uint32_t y[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, y[e] >> 16 & 0x7fffu));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^14 over the power of two in it, as the bits of an exponent
+      const int up = min(268 - (int)(top >> 7), 250);  // times 2 is finite still
+      const float times = __int_as_float(up << 23);
       float sum[G] = {};
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
-        const uint4 x = raw[nt][i];
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t y[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+        float x[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[i / 2] += scale_of(y[e]) + min_of(y[e]);
-        const uint32_t z[4] = {__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632)};
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = scale_of(y[e]);
+          x[2 * e + 1] = min_of(y[e]);
+          sum[i / 2] += x[2 * e] + x[2 * e + 1];
+        }
+        // dimensions e and e + 4 meet codes times 8, 4, 64 and 8 (2^-24)
+        constexpr float place[4] = {1.0f, 2.0f, 0.125f, 1.0f};
 #pragma unroll
-        for (int f = 0; f < F; ++f)
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t two = pack_half2(x[e] * (times * place[e]), x[e + 4] * (times * place[e]));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) qf[nt][f][i][e] = row_fold == f ? z[e] : 0u;
+          for (int f = 0; f < F; ++f) qf[nt][f][i][e] = row_fold == f ? two : 0u;
+        }
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        unit[nt][e] = __int_as_float(min(275 - __shfl_sync(0xffffffffu, up, (2 * t + e) * 4), 255) << 23);
 #pragma unroll
       for (int gi = 0; gi < G; ++gi) {
         sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 1);
         sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 2);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          qs[nt][gi][e] = __shfl_sync(0xffffffffu, sum[gi], (2 * t + e) * 4);
-          init[nt][gi][e] = init[nt][gi][e + 2] = -16.0f * qs[nt][gi][e];
-        }
+        for (int e = 0; e < 2; ++e) qs[nt][gi][e] = __shfl_sync(0xffffffffu, sum[gi], (2 * t + e) * 4);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) lim[nt][e] = kv4_seen(len, a.n, (col0 + nt * 8 + (2 * t + e) % CW) / group, a.causal);
@@ -298,8 +333,16 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
     // sums of a lane are of its own tokens until the end of the run
     float o[NT][G][4][4] = {};
     float m[NT][2], ref[NT][2] = {}, l[NT][2] = {}, off[NT][G][2] = {};  // ref: m score_scale, or 0 for none
+    float part[NT][G][2] = {};  // sums of P' not yet taken off o
+    float wide[NT][G][2];  // w of the comment above
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nt][e] = -INFINITY;
+#pragma unroll
+        for (int gi = 0; gi < G; ++gi) wide[nt][gi][e] = KVA_WIDEST;
+      }
 
     // One block of 64 tokens. WHOLE: every column sees all of them.
     auto block = [&](auto whole_tag, uint32_t blk, int key0) {
@@ -318,14 +361,19 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             uint32_t xa[4], xb[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              xa[e] = and_or<0x41804180u>(__funnelshift_r(ka[i], ka[i], 4 * e), mask);
-              xb[e] = and_or<0x41804180u>(__funnelshift_r(kb[i], kb[i], 4 * e), mask);
+              // the words are rotated left by 3: nibbles 0 (and 4) in bits 3 .. 6, and 5 bits
+              // on nibbles 1 in bits 2 .. 5 and 2 in bits 6 .. 9, and 12 bits on 3 in 3 .. 6
+              constexpr int shift[4] = {0, 5, 5, 12};
+              constexpr uint32_t mask[4] = {0x00780078u, 0x003c003cu, 0x03c003c0u, 0x00780078u};
+              xa[e] = __funnelshift_r(ka[i], ka[i], shift[e]) & mask[e];
+              xb[e] = __funnelshift_r(kb[i], kb[i], shift[e]) & mask[e];
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint32_t(&b)[4] = qf[nt][f][i];
               float(&d)[4] = acc[nt][i / 2];
-              mma16816(d, xa[0], xb[0], xa[1], xb[1], b[0], b[1], f == 0 && i % 2 == 0 ? init[nt][i / 2] : d);
+              float none[4] = {};
+              mma16816(d, xa[0], xb[0], xa[1], xb[1], b[0], b[1], f == 0 && i % 2 == 0 ? none : d);
               mma16816(d, xa[2], xb[2], xa[3], xb[3], b[2], b[3], d);
             }
           }
@@ -339,16 +387,17 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t(&p)[G] = e < 2 ? pa : pb;
-            float x = scale_of(p[0]) * acc[nt][0][e];
+            float x = scale_of(p[0]) * acc[nt][0][e], y = min_of(p[0]) * qs[nt][0][e & 1];
 #pragma unroll
-            for (int gi = 1; gi < G; ++gi) x = fmaf(scale_of(p[gi]), acc[nt][gi][e], x);
-#pragma unroll
-            for (int gi = 0; gi < G; ++gi) x = fmaf(min_of(p[gi]), qs[nt][gi][e & 1], x);
+            for (int gi = 1; gi < G; ++gi) {
+              x = fmaf(scale_of(p[gi]), acc[nt][gi][e], x);
+              y = fmaf(min_of(p[gi]), qs[nt][gi][e & 1], y);
+            }
+            x = fmaf(x, unit[nt][e & 1], y);
             if (!WHOLE && key0 + ra + (e >> 1) * 8 >= lim[nt][e & 1]) x = -INFINITY;
             s[j][nt][e] = x;
           }
       }
-      float ones[NT][G][4];  // sums of P' over the block
       if (a.scores != nullptr) {
         float* to = a.scores + ((long long)at.beta * a.d.kv_heads + kvh) * a.cols * a.d.capacity + key0 + token;
 #pragma unroll
@@ -386,16 +435,22 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
             for (int x = CW / 2; x < 32; x <<= 1)  // all lanes that hold this column or a copy of it
               now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
             const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx((m[nt][e] - now) * a.score_scale);
+            const float back = m[nt][e] == -INFINITY ? INFINITY : ex2_approx((now - m[nt][e]) * a.score_scale);
             m[nt][e] = now;
             ref[nt][e] = now == -INFINITY ? 0.f : now * a.score_scale;
             l[nt][e] *= f;
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) {
               off[nt][gi][e] *= f;
+              part[nt][gi][e] *= f;
+              // the P' so far fall by f: w rises by as much and their sum stays, as long as w can
+              float& w = wide[nt][gi][e];
+              const float more = w * back, now_o = more <= KVA_WIDEST ? 1.0f : __fdividef(KVA_WIDEST * f, w);
+              w = fminf(more, KVA_WIDEST);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                o[nt][gi][i][e] *= f;
-                o[nt][gi][i][e + 2] *= f;
+                o[nt][gi][i][e] *= now_o;
+                o[nt][gi][i][e + 2] *= now_o;
               }
             }
           }
@@ -410,7 +465,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         uint32_t bf[NT][G][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
+          float p[4], y[G][4], high = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             p[e] = ex2_approx(fmaf(s[j][nt][e], a.score_scale, -ref[nt][e & 1]));
@@ -418,23 +473,44 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
           }
 #pragma unroll
           for (int gi = 0; gi < G; ++gi) {
-            float x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t pr = e < 2 ? va[gi] : vb[gi];
-              const float mid = fmaf(7.5f, scale_of(pr), min_of(pr));
-              x[e] = p[e] * scale_of(pr);
+              y[gi][e] = p[e] * scale_of(pr);
               // a token that is not seen may have any parameters, NaN among them
               const bool live = WHOLE || key0 + ra + (e >> 1) * 8 < lim[nt][e & 1];
-              if (!live) x[e] = 0.f;
-              if (live) off[nt][gi][e & 1] = fmaf(p[e], mid, off[nt][gi][e & 1]);
+              if (!live) y[gi][e] = 0.f;
+              part[nt][gi][e & 1] += y[gi][e];
+              if (live) off[nt][gi][e & 1] = fmaf(p[e], fmaf(7.5f, scale_of(pr), min_of(pr)), off[nt][gi][e & 1]);
             }
-            bf[nt][gi][0] = transpose8(pack_bf16x2(x[0], x[1]));
-            bf[nt][gi][1] = transpose8(pack_bf16x2(x[2], x[3]));
-            float none[4] = {};
-            mma16816(ones[nt][gi], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, bf[nt][gi][0], bf[nt][gi][1],
-                     j == 0 ? none : ones[nt][gi]);
+            high = max3f(high, y[gi][0] * wide[nt][gi][0], y[gi][1] * wide[nt][gi][1]);
+            high = max3f(high, y[gi][2] * wide[nt][gi][0], y[gi][3] * wide[nt][gi][1]);
           }
+          if (__any_sync(0xffffffffu, high > KVA_HIGH)) {
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float top = fmaxf(y[gi][e], y[gi][e + 2]);
+#pragma unroll
+                for (int x = CW / 2; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                float& w = wide[nt][gi][e];
+                if (top * w > KVA_HIGH) {  // the power of two that takes it to 2^7
+                  const float less = __int_as_float((261 - (__float_as_int(top) >> 23)) << 23), now_o = __fdividef(less, w);
+                  w = less;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    o[nt][gi][i][e] *= now_o;
+                    o[nt][gi][i][e + 2] *= now_o;
+                  }
+                }
+              }
+          }
+#pragma unroll
+          for (int gi = 0; gi < G; ++gi)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              bf[nt][gi][x] = transpose8(pack_half2(y[gi][2 * x] * wide[nt][gi][0], y[gi][2 * x + 1] * wide[nt][gi][1]));
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) {
@@ -454,7 +530,8 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
               for (int x = 0; x < 2; ++x) b[nt][x] = F == 1 || row_fold == f ? bf[nt][gi][x] : 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              auto code = [&](uint32_t x) { return and_or<0x41804180u>(i == 0 ? x << 3 : x >> (4 * i - 3), mask); };
+              // nibbles 0 and 2 in bits 0 .. 3, 1 and 3 (times 16) in bits 4 .. 7
+              auto code = [&](uint32_t x) { return x >> (i / 2 * 8) & (i % 2 ? 0x00f000f0u : 0x000f000fu); };
               const uint32_t a0 = code(lo0), a1 = code(hi0), a2 = code(lo1), a3 = code(hi1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][gi][i], a0, a1, a2, a3, b[nt][0], b[nt][1], o[nt][gi][i]);
@@ -462,14 +539,34 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
           }
         }
       }
+    };
+
+    auto over_lanes = [](float x) {  // of a column and its copies
+#pragma unroll
+      for (int y = CW / 2; y < 32; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
+      return x;
+    };
+    auto over_copies = [](float x) {
+#pragma unroll
+      for (int y = CW / 2; y < 4; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
+      return x;
+    };
+    auto centre = [&]() {  // takes 7.5 sum P' off o (off its first copy)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int gi = 0; gi < G; ++gi)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int e = 0; e < 2; ++e) {
+            const float all = over_lanes(part[nt][gi][e]) * wide[nt][gi][e];
+            part[nt][gi][e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][gi][i][e] = fmaf(-23.5f, ones[nt][gi][e & 1], o[nt][gi][i][e]);
+            for (int i = 0; i < 4; ++i) {
+              const float x = fold == 0 ? all * (i % 2 ? -7.5f * 0x1p-20f : -7.5f * 0x1p-24f) : 0.f;
+              o[nt][gi][i][e] += x;
+              o[nt][gi][i][e + 2] += x;
+            }
+          }
     };
 
     const int piece = min(at.nb - at.blk, at.left);
@@ -493,22 +590,13 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       __syncwarp();  // every lane has read the stage
       ++done;
       issue();
+      if (k % KVA_CENTRE == KVA_CENTRE - 1) centre();
     }
 
     if (lost) break;
 
-    // the run's sums for this segment: over the lanes of a column and its copies
+    // the run's sums for this segment
     const long long slot = (long long)at.beta * rows + at.row + w;
-    auto over_lanes = [](float x) {
-#pragma unroll
-      for (int y = CW / 2; y < 32; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
-      return x;
-    };
-    auto over_copies = [](float x) {
-#pragma unroll
-      for (int y = CW / 2; y < 4; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
-      return x;
-    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,12 +608,13 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         if (real && g == 0) (DIRECT ? own_ml + c : a.part_ml + to)[0] = make_float2(m[nt][e] * a.score_scale, sum);
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
-          const float add = over_lanes(off[nt][gi][e]);
+          const float add = over_lanes(fmaf(-7.5f, part[nt][gi][e], off[nt][gi][e]));
           float x[8];  // dimensions 8u .. 8u + 7 of word u = 8 gi + g
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[i] = over_copies(o[nt][gi][i][e]) + add;
-            x[i + 4] = over_copies(o[nt][gi][i][e + 2]) + add;
+            const float unit = i % 2 ? 0x1p20f : 0x1p24f, per = 1.0f / wide[nt][gi][e];
+            x[i] = fmaf(over_copies(o[nt][gi][i][e]) * unit, per, add);
+            x[i + 4] = fmaf(over_copies(o[nt][gi][i][e + 2]) * unit, per, add);
           }
           if (real) {
             float4* dst = reinterpret_cast<float4*>((DIRECT ? own_o + c * DH : a.part_o + to * DH) + (gi * 8 + g) * 8);

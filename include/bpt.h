@@ -540,8 +540,10 @@ int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, c
  * lse2: fp32 [b, heads, n] as of bpt_attention_lse, or NULL. weights: fp32 [b,
  * kv_heads, capacity], or NULL: every place's softmax weight, summed over the
  * new tokens and the heads that share it, is ADDED to it (places at or past
- * lens[beta] are left as they are). The scores and all sums are fp32; the
- * softmax weights enter the product with V as bf16, times the scale of V.
+ * lens[beta] are left as they are). The scores and all sums are fp32. q (below
+ * 2^120) enters its products as fp16, relative to its largest element; so does
+ * each softmax weight times a token's scale of V, relative to the largest such
+ * product of the column and its 64 dimensions, of which 2^-31 is lost.
  * workspace: bpt_kv4_attention_workspace_bytes of the same arguments, which may
  * be 0 (short caches without weights; workspace may then be NULL). */
 size_t bpt_kv4_attention_workspace_bytes(int b, int n, int heads, int kv_heads, int capacity, int dh,

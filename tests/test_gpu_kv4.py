@@ -9,9 +9,9 @@ Attention, per query (c = log2(e) / sqrt(dh)):
   and logarithm, in relation to its size 2^-23;
 * a weight p by p (2 ln2 E + 2^-19), and their sum over the queries by an
   fp32 rounding each;
-* o: each p's product with V's scale is rounded to bf16, 2^-8 of p scale
-  |code - 7.5| at most 7.5 p scale, the result to bf16, 2^-8 of |o|, and the
-  weights' error shows as (2 ln2 E + 2^-18) sum p |V|.
+* o: each p's product with V's scale is rounded to fp16, 2^-11 of p scale code,
+  at most 15 p scale, the result to bf16, 2^-8 of |o|, and the weights' error
+  shows as (2 ln2 E + 2^-18) sum p (|min| + 15 scale).
 """
 
 import numpy as np
@@ -181,8 +181,9 @@ def check_attention(q, cache, held, lens, heads, causal=True, weights=None, **kw
         seen = np.arange(lens[i]) < (lens[i] - n + 1 + np.arange(n) if causal else np.full(n, lens[i]))[:, None]
         p = np.where(seen, np.exp2(s * np.log2(np.e) - np.where(live, rl, 0)[..., None]), 0)  # [heads, n, len]
         step = np.repeat(one["vs"], 64, -1)[hh]
-        tol = (2.0 ** -8 * (np.einsum("hnu,hud->nhd", p, 7.5 * step) + np.abs(ro))
-               + (2 * np.log(2) * E.T[..., None] + 2.0 ** -18) * np.einsum("hnu,hud->nhd", p, np.abs(one["v"])[hh]) + 1e-30)
+        most = np.repeat(np.abs(one["vm"]) + 15 * one["vs"], 64, -1)[hh]
+        tol = (2.0 ** -11 * np.einsum("hnu,hud->nhd", p, 15 * step) + 2.0 ** -8 * np.abs(ro)
+               + (2 * np.log(2) * E.T[..., None] + 2.0 ** -18) * np.einsum("hnu,hud->nhd", p, most) + 1e-30)
         err = np.abs(on[i] - ro)
         assert (err <= tol).all(), f"o is {(err / tol).max():.2f} times its bound off"
         if weights is not None:
@@ -236,7 +237,58 @@ def test_attention_with_large_and_equal_scores():
         q[:, :, dh:] = 0
         o = check_attention(q, cache, held, [150], 2, causal=False)
         mean = held[0]["v"][0].mean(0)
-        assert (np.abs(heads_of(o, 2)[0, 0, 1] - mean) <= 2.0 ** -8 * (np.abs(mean) + 7.5 * held[0]["vs"].max())).all()
+        assert (np.abs(heads_of(o, 2)[0, 0, 1] - mean) <= 2.0 ** -8 * np.abs(mean) + 2.0 ** -11 * 15 * held[0]["vs"].max()).all()
+
+
+@pytest.mark.parametrize("capacity", [512, 20032])
+@pytest.mark.parametrize("pattern", ["alternating", "large and unseen first", "large and unseen last", "rising", "falling",
+                                     "tiny", "huge"])
+def test_values_of_very_different_size(pattern, capacity):
+    # V's rows scaled by powers of two, and scores (K's rows are constant) that
+    # raise the small ones. What lies 2^-31 below the largest product of weight
+    # and scale may be lost.
+    n, dh = 400, 128
+    t = np.arange(n)
+    size, score = {"alternating": (np.where(t % 2, 30, -30), 0 * t),
+                   "large and unseen first": (np.where(t < 70, 60, 0), np.where(t < 70, -150, 0)),
+                   "large and unseen last": (np.where(t < 330, 0, 60), np.where(t < 330, 0, -150)),
+                   "rising": (t // 8, -t // 16), "falling": (-(t // 8), t // 16),
+                   "tiny": (0 * t - 90, 0 * t), "huge": (0 * t + 100, 0 * t)}[pattern]
+    g = np.random.default_rng(5)
+    v = torch.tensor(g.standard_normal((1, n, dh)) * 2.0 ** size[:, None]).float().bfloat16().cuda()
+    k = torch.tensor(np.broadcast_to(score[:, None] / np.sqrt(dh), (n, dh))[None].copy()).float().bfloat16().cuda()
+    q = torch.ones((1, 1, dh), dtype=torch.bfloat16, device="cuda")
+    cache = bpt.kv4_cache(1, 1, capacity, dh)
+    bpt.kv4_store(cache, k, v, ints(0))
+    o = heads_of(bpt.kv4_attention(q, cache, ints(n), 1), 1)[0, 0, 0]
+    kc, vc = (so.quantise(heads_of(x, 1)[0, :, 0]) for x in (k, v))
+    s = so.values(*kc) @ np.ones(dh) / np.sqrt(dh)
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    step, low = np.repeat(vc[1], 64, -1), np.repeat(vc[2], 64, -1)
+    ref = p @ so.values(*vc)
+    E = (dh + 16) * 2.0 ** -24 * np.log2(np.e) / np.sqrt(dh) * dh * np.abs(so.values(*kc)).max()
+    tol = (2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * np.log(2) * E + 2.0 ** -18) * (p @ (np.abs(low) + 15 * step))
+           + n * 2.0 ** -31 * 15 * (p[:, None] * step).max(0))
+    assert (np.abs(o - ref) <= tol).all(), f"{(np.abs(o - ref) / tol).max():.2f} times the bound"
+    assert bpt.stream_status() == 0
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("size", [-120, -60, 60, 110])
+def test_queries_of_any_size(size, dh):
+    # scores of the usual size from very large or small queries on keys of the inverse size
+    cache = bpt.kv4_cache(1, 1, 256, dh)
+    g = np.random.default_rng(6)
+    k = torch.tensor(g.standard_normal((1, 150, dh)) * 2.0 ** -size).float().bfloat16().cuda()
+    q = torch.tensor(g.standard_normal((1, 1, dh)) * 2.0 ** size).float().bfloat16().cuda()
+    v = bf16((1, 150, dh), 7)
+    bpt.kv4_store(cache, k, v, ints(0))
+    one = {}
+    for name, x in (("k", k), ("v", v)):
+        codes, scale, low = so.quantise(heads_of(x, 1)[0].transpose(1, 0, 2))
+        one[name], one[name + "s"], one[name + "m"] = so.values(codes, scale, low), scale, low
+    check_attention(q, cache, [one], [150], 1)
 
 
 @pytest.mark.parametrize("dh", [64, 128])
