@@ -244,8 +244,9 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_load_kernel(const __grid_cons
   if (t >= a.n) return;
   for (int beta = blockIdx.y; beta < a.d.b; beta += gridDim.y) {
     const int len = clamp_count(a.lens[beta], a.d.capacity, a.status);
-    const long long at = (a.start == nullptr ? 0LL : (long long)a.start[beta]) + t;
-    if (at < 0) record_range(a.status);
+    const int first = a.start == nullptr ? 0 : a.start[beta];
+    if (first < 0 || first > a.d.capacity) record_range(a.status);
+    const long long at = (long long)first + t;
     uint32_t x[2][8] = {};
     if (at >= 0 && at < len) {
       const int r = at % KV4_BLOCK;

@@ -257,7 +257,7 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
   int sms = 0;
   BPT_TRY(check_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((a.tokens + a.tile - 1) / a.tile, (a.units + a.chunk - 1) / a.chunk);
+  const dim3 grid((unsigned)(((long long)a.tokens + a.tile - 1) / a.tile), (a.units + a.chunk - 1) / a.chunk);
   {
     LaunchScope ls("rotary", st);
     if (es == 2 && w == 8)

@@ -149,6 +149,10 @@ def test_places_outside_the_cache_are_dropped_and_reported():
     k, _ = bpt.kv4_load(cache, ints(64, 64, 65), 2, start=ints(63, -1, 2 ** 31 - 1))
     assert bpt.stream_status() == RANGE
     assert (k[0, 1] == 0).all() and (k[1, 0] == 0).all() and (k[2] == 0).all() and (k[1, 1] != 0).any()
+    bpt.kv4_load(cache, ints(64, 64, 64), 2, start=ints(0, 65, 0))
+    assert bpt.stream_status() == RANGE
+    bpt.kv4_load(cache, ints(64, 64, 64), 2, start=ints(0, 64, 63))  # past the length, but inside
+    assert bpt.stream_status() == 0
     o, lse2 = bpt.kv4_attention(x[:, :1].contiguous(), cache, ints(65, -3, 64), 1, return_lse=True)
     assert bpt.stream_status() == RANGE
     full, _ = bpt.kv4_attention(x[:, :1].contiguous(), cache, ints(64, 0, 64), 1, return_lse=True)
@@ -349,6 +353,44 @@ def test_strided_queries_streams_and_graphs():
     ref = bpt.kv4_attention(q, cache, ln, heads, weights=w2)
     bpt.kv4_attention(q, cache, ln, heads, weights=w2)
     assert torch.equal(outs[0], ref) and torch.equal(outs[1], ref) and torch.equal(w, w2)
+
+
+@pytest.mark.parametrize("capacity", [256, 20032])
+def test_a_captured_step_and_eviction(capacity):
+    # one decoded token (positions, store, attention with weights, the new length) and an eviction, captured and
+    # replayed on new queries, against the same calls made one by one
+    b, heads, kv, dh, keep = 2, 4, 2, 64, 40
+    lens = [130, 77]
+    base, _ = filled(b, kv, dh, lens, capacity, seed=31)
+    freq, _ = bpt.rotary_frequencies(dh)
+    rows = bf16((b, 1, (heads + 2 * kv) * dh), 32)
+
+    def step(cache, small, ln, w):
+        q, k = bpt.rotary(rows[..., :heads * dh], rows[..., heads * dh:(heads + kv) * dh], heads, kv, freq,
+                          positions=ln.view(b, 1))
+        bpt.kv4_store(cache, k, rows[..., (heads + kv) * dh:], ln)
+        ln += 1
+        o, lse2 = bpt.kv4_attention(q, cache, ln, heads, weights=w, return_lse=True)
+        return (o, lse2, *bpt.kv4_evict(cache, w, ln, keep, 7, small), *bpt.kv4_load(small, ln.clamp(max=keep), keep))
+
+    def state():
+        return (bpt.KV4Cache(base.data.clone(), dh), bpt.kv4_cache(b, kv, keep, dh), ints(*lens),
+                torch.zeros((b, kv, capacity), device="cuda"))
+
+    step(*state())  # loads what a capture must not load
+    one, two = state(), state()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*one)
+    for new in range(3):
+        rows.copy_(bf16(rows.shape, 40 + new))
+        graph.replay()
+        ref = step(*two)
+        torch.cuda.synchronize()
+        for x, y in zip((*out, *one[2:]), (*ref, *two[2:])):
+            assert torch.equal(x, y)
+        assert torch.equal(one[0].data, two[0].data) and torch.equal(one[1].data, two[1].data)
+    assert bpt.stream_status() == 0
 
 
 def test_two_streams_at_once():
