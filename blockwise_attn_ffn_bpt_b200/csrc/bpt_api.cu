@@ -228,8 +228,7 @@ int check_device(int* sms) {
                    cudaFuncSetAttribute(attention_bwd_tcgen05<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         AttnBwdCfg<128>::SMEM_BYTES) == cudaSuccess &&
                    kva_set_attributes() &&
-                   cudaFuncSetAttribute(kv4_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        EVICT_CACHED * 4) == cudaSuccess &&
+                   evict_set_attributes() &&
                    cudaFuncSetAttribute(layer_mega_tcgen05<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         mega_smem_bytes<64>()) == cudaSuccess &&
                    cudaFuncSetAttribute(layer_mega_tcgen05<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,

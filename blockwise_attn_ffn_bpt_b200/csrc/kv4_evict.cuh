@@ -9,16 +9,18 @@
 // their order alone, so the result does not depend on any order of the atomics.
 #pragma once
 
+#include "gemm_pair.cuh"  // cluster rank, barrier and addresses
 #include "kv4_cache.cuh"
 
 namespace bpt {
 
 constexpr int EVICT_THREADS = 1024;
 constexpr int EVICT_BINS = 2048;
-// Copies of the histogram, one to every fourth lane: weights of a few octaves
-// share few bins of the first digit, and lanes that add to one bin take turns.
-constexpr int EVICT_COPIES = 4;
-constexpr int EVICT_CACHED = 49152;  // tokens whose keys fit in shared memory (192 KB)
+// Copies of the histogram, one to every second or fourth lane: weights of a few
+// octaves share few bins of the first digit, and lanes that add to one bin take
+// turns. (48 KB of it and of the cluster's totals are there without asking.)
+constexpr int evict_copies(int cl) { return cl > 1 ? 2 : 4; }
+constexpr int EVICT_CACHED = 40960;  // tokens of a block whose keys stay in shared memory (160 KB)
 
 struct Kv4SelectArgs {
   const float* weights;  // [b, kv_heads, capacity]
@@ -29,6 +31,18 @@ struct Kv4SelectArgs {
   int* lens_out;         // [b]
   int* status;
 };
+
+// Shared memory of the cluster's block r.
+__device__ __forceinline__ int cluster_load(uint32_t addr, int r) {
+  int x;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(mapa_shared(addr, (uint32_t)r)) : "memory");
+  return x;
+}
+__device__ __forceinline__ int2 cluster_load2(uint32_t addr, int r) {
+  int2 x;
+  asm volatile("ld.shared::cluster.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(mapa_shared(addr, (uint32_t)r)) : "memory");
+  return x;
+}
 
 // A weight as a whole number of the same order; both zeros are equal, and NaN
 // is the heaviest.
@@ -44,35 +58,45 @@ __device__ __forceinline__ uint4 weight_keys(const float4& w, int i, int old) {
                     i + 2 < old ? weight_key(w.z) : 0u, i + 3 < old ? weight_key(w.w) : 0u);
 }
 
-// One block a (sequence, head). The keys of up to EVICT_CACHED tokens stay in
-// shared memory after the first pass; longer rows are read again, from L2.
-template <bool CACHED>
+// A cluster of CL blocks a (sequence, head), each with an equal part of its
+// tokens. The keys of up to EVICT_CACHED tokens a block stay in shared memory
+// after the first pass; longer rows are read again, from L2.
+template <int CL, bool CACHED>
 __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_constant__ Kv4SelectArgs a) {
   extern __shared__ uint4 cached[];
-  __shared__ int hist[EVICT_COPIES][EVICT_BINS];
+  constexpr int COPIES = evict_copies(CL);
+  __shared__ int hist[COPIES][EVICT_BINS];
   __shared__ int warp_sum[32], warp_tie[32];
   __shared__ int s_bin, s_need, s_count;
+  // what the other blocks of the cluster read: the histogram (by turns, so that
+  // one barrier a pass will do) and the block's counts of the last step
+  __shared__ alignas(8) int s_total[CL > 1 ? 2 : 1][CL > 1 ? EVICT_BINS : 1];
+  __shared__ int s_above, s_ties;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CL > 1 ? (int)cluster_ctarank() : 0;
   const int rows = a.d.b * a.d.kv_heads;
   grid_dependents_start();
-  for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+  for (int row = blockIdx.x / CL; row < rows; row += gridDim.x / CL) {
     const int beta = row / a.d.kv_heads;
     const int len = clamp_count(a.lens[beta], a.d.capacity, a.status);
     const int left = min(len, a.keep), recent = min(a.recent, left);
     const int old = len - recent, need = left - recent;  // choose `need` of the `old` first tokens
     const float* w = a.weights + (long long)row * a.d.capacity;
     int* kept = a.kept + (long long)row * a.keep;
-    if (tid == 0 && row == beta * a.d.kv_heads) a.lens_out[beta] = left;
-    for (int i = need + tid; i < a.keep; i += EVICT_THREADS) kept[i] = i < left ? old + i - need : -1;
+    if (rank == 0 && tid == 0 && row == beta * a.d.kv_heads) a.lens_out[beta] = left;
+    const int first = rank * EVICT_THREADS + tid;
+    for (int i = need + first; i < a.keep; i += CL * EVICT_THREADS) kept[i] = i < left ? old + i - need : -1;
     if (need == old) {
-      for (int i = tid; i < need; i += EVICT_THREADS) kept[i] = i;
+      for (int i = first; i < need; i += CL * EVICT_THREADS) kept[i] = i;
       continue;
     }
     if (need == 0) continue;
-    const int quads = (old + 3) / 4;
-    auto keys_of = [&](int i, bool first) -> uint4 {
-      if (CACHED && !first) return cached[i];
-      const uint4 k = weight_keys(__ldg(reinterpret_cast<const float4*>(w) + i), 4 * i, old);
+    // this block's part, in groups of 4 tokens
+    const int every = (old + 3) / 4, share = (every + CL - 1) / CL, quad0 = min(rank * share, every);
+    const int quads = min(share, every - quad0);
+    auto keys_of = [&](int i, bool read) -> uint4 {
+      if (CACHED && !read) return cached[i];
+      const uint4 k = weight_keys(__ldg(reinterpret_cast<const float4*>(w) + quad0 + i), 4 * (quad0 + i), old);
       if (CACHED) cached[i] = k;
       return k;
     };
@@ -83,10 +107,10 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       const uint32_t digit = (1u << bits) - 1;
       __syncthreads();
-      for (int i = tid; i < EVICT_COPIES * EVICT_BINS; i += EVICT_THREADS) (&hist[0][0])[i] = 0;
+      for (int i = tid; i < COPIES * EVICT_BINS; i += EVICT_THREADS) (&hist[0][0])[i] = 0;
       __syncthreads();
       auto count = [&](uint32_t key) {
-        if ((key & mask) == prefix) atomicAdd(&hist[lane % EVICT_COPIES][(key >> shift) & digit], 1);
+        if ((key & mask) == prefix) atomicAdd(&hist[lane % COPIES][(key >> shift) & digit], 1);
       };
 #pragma unroll 4
       for (int i = tid; i < quads; i += EVICT_THREADS) {
@@ -98,11 +122,25 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
       }
       __syncthreads();
       // from the top: thread i holds bins BINS - 1 - 2i and BINS - 2 - 2i
+      const int top = EVICT_BINS - 1 - 2 * tid;
       int hi = 0, lo = 0;
 #pragma unroll
-      for (int x = 0; x < EVICT_COPIES; ++x) {
-        hi += hist[x][EVICT_BINS - 1 - 2 * tid];
-        lo += hist[x][EVICT_BINS - 2 - 2 * tid];
+      for (int x = 0; x < COPIES; ++x) {
+        hi += hist[x][top];
+        lo += hist[x][top - 1];
+      }
+      if constexpr (CL > 1) {
+        int* mine = s_total[pass & 1];
+        mine[top] = hi;
+        mine[top - 1] = lo;
+        cluster_sync_all();
+        hi = lo = 0;
+#pragma unroll
+        for (int r = 0; r < CL; ++r) {
+          const int2 x = cluster_load2(smem_addr(mine + top - 1), r);
+          lo += x.x;
+          hi += x.y;
+        }
       }
       int sum = hi + lo;
 #pragma unroll
@@ -149,6 +187,17 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
     __syncthreads();
     int above = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
     int ties = __reduce_add_sync(0xffffffffu, lane < warp ? warp_tie[lane] : 0);
+    if constexpr (CL > 1) {
+      if (tid == EVICT_THREADS - 1) {
+        s_above = above + more;
+        s_ties = ties + tie;
+      }
+      cluster_sync_all();
+      for (int r = 0; r < rank; ++r) {
+        above += cluster_load(smem_addr(&s_above), r);
+        ties += cluster_load(smem_addr(&s_ties), r);
+      }
+    }
     const uint32_t below = (1u << lane) - 1;
     if (want == 0) {  // no ties to choose from
       for (int i0 = lo; i0 < hi; i0 += 32) {
@@ -158,10 +207,10 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
         const uint32_t b0 = __ballot_sync(0xffffffffu, s0), b1 = __ballot_sync(0xffffffffu, s1);
         const uint32_t b2 = __ballot_sync(0xffffffffu, s2), b3 = __ballot_sync(0xffffffffu, s3);
         int at = above + __popc(b0 & below) + __popc(b1 & below) + __popc(b2 & below) + __popc(b3 & below);
-        if (s0) kept[at++] = 4 * i;
-        if (s1) kept[at++] = 4 * i + 1;
-        if (s2) kept[at++] = 4 * i + 2;
-        if (s3) kept[at] = 4 * i + 3;
+        if (s0) kept[at++] = 4 * (quad0 + i);
+        if (s1) kept[at++] = 4 * (quad0 + i) + 1;
+        if (s2) kept[at++] = 4 * (quad0 + i) + 2;
+        if (s3) kept[at] = 4 * (quad0 + i) + 3;
         above += __popc(b0) + __popc(b1) + __popc(b2) + __popc(b3);
       }
     } else {
@@ -183,14 +232,41 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (is_above[e] || (is_tie[e] && tied < want)) kept[at + min(tied, want)] = 4 * i + e;
+          if (is_above[e] || (is_tie[e] && tied < want)) kept[at + min(tied, want)] = 4 * (quad0 + i) + e;
           at += is_above[e];
           tied += is_tie[e];
         }
       }
     }
-    __syncthreads();
+    if constexpr (CL > 1)
+      cluster_sync_all();  // no block ends, or starts on its next row, before the others have read its counts
+    else
+      __syncthreads();
   }
+}
+
+// Blocks of a cluster: more where a row is long and the rows alone leave SMs
+// idle (two blocks on an SM gain nothing). Device time, 1 against 2 and 4 blocks:
+// 4 rows of 8192 tokens 11.3, 12.4, 12.3 us, of 32768 tokens 18.8, 15.8, 14.8, 2
+// rows of 131072 tokens 69, 42, 22; 64 rows of 32768 tokens 23.9, 20.0, 30.7.
+inline int evict_cluster(long long rows, int capacity) {
+  if (capacity < 16384) return 1;
+  return rows * 4 <= KVA_MAX_SMS ? 4 : rows * 2 <= KVA_MAX_SMS ? 2 : 1;
+}
+
+typedef void (*EvictKernel)(const Kv4SelectArgs);
+inline EvictKernel evict_kernel(int cl, bool cached) {
+  if (cl == 4) return cached ? kv4_select_kernel<4, true> : kv4_select_kernel<4, false>;
+  if (cl == 2) return cached ? kv4_select_kernel<2, true> : kv4_select_kernel<2, false>;
+  return cached ? kv4_select_kernel<1, true> : kv4_select_kernel<1, false>;
+}
+
+inline bool evict_set_attributes() {
+  bool ok = true;
+  for (int cl : {1, 2, 4})
+    ok = ok && cudaFuncSetAttribute(evict_kernel(cl, true), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    EVICT_CACHED * 4) == cudaSuccess;
+  return ok;
 }
 
 struct Kv4MoveArgs {

@@ -101,6 +101,24 @@ int launch_dependent(void (*kernel)(const Args), const Args& args, dim3 grid, un
   return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
 }
 
+// Launches a kernel in clusters of `cl` blocks.
+template <typename Args>
+int launch_cluster(void (*kernel)(const Args), const Args& args, dim3 grid, unsigned threads, int cl, size_t smem,
+                   cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cl;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+}
+
 unsigned grid_y(long long rows) { return (unsigned)std::min<long long>(rows, 65535); }
 
 template <typename T, int W>
@@ -465,10 +483,11 @@ int bpt_kv4_evict(const void* cache, const float* weights, const int* lens, int 
   {
     LaunchScope ls("kv4_select", st);
     const Kv4SelectArgs a{weights, d, lens, keep, recent, kept, lens_out, status};
-    if (capacity <= EVICT_CACHED)
-      kv4_select_kernel<true><<<(unsigned)rows, EVICT_THREADS, (size_t)capacity * 4, st>>>(a);
-    else
-      kv4_select_kernel<false><<<(unsigned)rows, EVICT_THREADS, 0, st>>>(a);
+    const int cl = evict_cluster((long long)rows, capacity);
+    const size_t share = (size_t)(capacity / 4 + cl - 1) / cl * 4;  // tokens of a block
+    const bool cached = share <= EVICT_CACHED;
+    BPT_TRY(launch_cluster(evict_kernel(cl, cached), a, dim3((unsigned)rows * cl), EVICT_THREADS, cl,
+                           cached ? share * 4 : 0, st));
   }
   {
     LaunchScope ls("kv4_move", st);

@@ -408,17 +408,17 @@ def test_two_streams_at_once():
     assert all(bpt.stream_status(s) == 0 for s in streams)
 
 
-def check_evict(dh, kv, lens, capacity, keep, recent, out_capacity, weights):
+def check_evict(dh, kv, lens, capacity, keep, recent, out_capacity, weights, rows=True):
     b = len(lens)
     cache = bpt.kv4_cache(b, kv, capacity, dh)
-    cache.data.copy_(torch.randint(0, 256, cache.data.shape, generator=torch.Generator().manual_seed(3)).byte())
+    cache.data.random_(0, 256, generator=torch.Generator(device="cuda").manual_seed(3))
     out = bpt.kv4_cache(b, kv, out_capacity, dh)
     out.data.fill_(0x5A)
     kept, new, moved = bpt.kv4_evict(cache, weights, ints(*lens), keep, recent, out)
     assert bpt.stream_status() == 0
     assert new.tolist() == [min(x, keep) for x in lens]
     wn, mn, kn = weights.cpu().numpy(), moved.cpu().numpy(), kept.cpu().numpy()
-    src, dst = cache.data.cpu().numpy(), out.data.cpu().numpy()
+    src, dst = (cache.data.cpu().numpy(), out.data.cpu().numpy()) if rows else (None, None)
     half, par = dh // 2, dh // 64 * 4
     v_at = 64 * (half + par)
 
@@ -435,6 +435,8 @@ def check_evict(dh, kv, lens, capacity, keep, recent, out_capacity, weights):
             ref = so.kept_tokens(wn[i, h], lens[i], keep, recent)
             assert kn[i, h].tolist() == ref + [-1] * (keep - len(ref))
             assert np.array_equal(mn[i, h, :len(ref)], wn[i, h, ref], equal_nan=True) and (mn[i, h, len(ref):] == 0).all()
+            if not rows:
+                continue
             for j, r in enumerate(ref):
                 assert np.array_equal(row(dst[i, h], j), row(src[i, h], r))
             for j in range(len(ref), out_capacity):
@@ -460,12 +462,23 @@ def test_evict_ties_signs_infinities_and_nan():
         check_evict(64, 1, [320, 300, 317], 320, keep, 2, 320, w.cuda())
 
 
-@pytest.mark.parametrize("length", [1023, 1025, 5000, 33333])
-def test_evict_from_long_caches(length):
+@pytest.mark.parametrize("length,heads", [(1023, 2), (1025, 2), (5000, 2), (33333, 2), (16390, 40), (16390, 80),
+                                          (200001, 1)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_from_long_caches(length, heads, ties):
+    # one, two and four blocks a row, keys in shared memory or not; few values let ties reach across every part
     g = torch.Generator().manual_seed(length)
     capacity = (length + 63) // 64 * 64
-    w = (torch.rand((1, 2, capacity), generator=g) * 50).round().cuda()  # few values: ties reach across every part
-    check_evict(64, 2, [length], capacity, 700, 33, 704, w)
+    w = torch.rand((1, heads, capacity), generator=g) * 50
+    w = (w.round() if ties else w).cuda()
+    check_evict(64, heads, [length], capacity, 300, 33, 320, w, rows=ties)
+
+
+def test_evict_without_shared_memory_for_the_keys():
+    # 150 rows fill the device with one block each; 45000 tokens are more than a block keeps
+    g = torch.Generator().manual_seed(3)
+    w = (torch.rand((1, 150, 45056), generator=g) * 50).cuda()
+    check_evict(64, 150, [45001], 45056, 100, 3, 128, w, rows=False)
 
 
 def test_a_run_of_them_together():
