@@ -138,7 +138,10 @@ __device__ __forceinline__ void load_stream32(const void* p, uint32_t (&x)[8]) {
 }
 
 // A thread takes 16 dimensions of K and of V of one token and head: 32 bytes
-// in, two words out of each. Bound by HBM.
+// in, two words out of each. 4 x 8192 tokens of 16 heads of 128 (343 MB in and
+// out, 52 us at the copy's rate): 65 us, 5.3 TB/s. Bound by the issue of its
+// instructions (72% of the slots) close behind the memory: 8 dimensions a thread
+// took 105 us, unpacked arithmetic and two divisions a group 69.
 template <int DH, bool WIDE>
 __global__ void __launch_bounds__(KV4_THREADS) kv4_store_kernel(const __grid_constant__ Kv4StoreArgs a) {
   constexpr int U = DH / 16;
@@ -231,8 +234,9 @@ __device__ __forceinline__ void store_stream32(void* p, const uint32_t (&x)[8]) 
 }
 
 // The store's mapping the other way round: 16 dimensions of K and V a thread.
-// Bound by HBM (its writes). The outputs' rows are 128 bytes or more, so every
-// 32 bytes are aligned where their start is (WIDE).
+// Bound by HBM (its writes): 60 us, 5.7 TB/s, at the store's example. The outputs'
+// rows are 128 bytes or more, so every 32 bytes are aligned where their start is
+// (WIDE).
 template <int DH, bool WIDE>
 __global__ void __launch_bounds__(KV4_THREADS) kv4_load_kernel(const __grid_constant__ Kv4LoadArgs a) {
   constexpr int U = DH / 16;
