@@ -1,15 +1,15 @@
 """Python binding of the B200 BPT layer-forward library (libbpt.so).
 
-Argument marshalling only: every step of the layer runs in the library's CUDA
-kernels. torch is used for device memory and streams. There is no fallback:
-if the built library is missing, or a call returns an error status, these
-functions raise.
+Argument marshalling only: every step runs in the library's CUDA kernels. torch
+is used for device memory and streams. The layer's entry points go through
+ctypes, those of a token-by-token loop through csrc/binding.cpp. There is no
+fallback: if a built library is missing, or a call returns an error status,
+these functions raise.
 """
 
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -465,54 +465,31 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", 
     return freq, magnitude.value
 
 
-def _rows(t: torch.Tensor, name: str, width: int, dtypes, like: Optional[torch.Tensor] = None) -> tuple:
-    """(pointer, elements between sequences, elements between tokens) of a CUDA
-    tensor [b, s, width] whose rows are contiguous."""
-    shape, stride, dtype = t.shape, t.stride(), t.dtype
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {dtype}")
-    if len(shape) != 3 or shape[2] != width:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [b, s, {width}]")
-    if like is not None and (shape[0] != like.shape[0] or shape[1] != like.shape[1] or dtype != like.dtype
-                             or t.get_device() != like.get_device()):
-        raise ValueError(f"{name} must have the tokens, dtype and device of the first tensor")
-    if stride[2] != 1:
-        raise ValueError(f"{name}'s rows must be contiguous")
-    return t.data_ptr(), stride[0], stride[1]
+_fast = None
 
 
-def _new_rows(like: torch.Tensor, b: int, s: int, width: int) -> tuple:
-    """A new contiguous tensor [b, s, width], the shape of `like`, and its place as of _rows."""
-    t = torch.empty_like(like) if like.is_contiguous() else torch.empty(b, s, width, dtype=like.dtype, device=like.device)
-    return t, (t.data_ptr(), s * width, width)
+def _load_binding():
+    """The C++ part of the binding (csrc/binding.cpp); raises if it has not been built."""
+    global _fast
+    if _fast is None:
+        lib()
+        from . import _binding as module
+        _fast = module
+    return _fast
 
 
-class _On:
-    """The given stream's device and stream as torch's current ones, so that
-    outputs and workspaces belong to the stream that uses them; by default the
-    tensors' device and its current stream. Enters as the stream's handle."""
+def _done(result, what: str):
+    """A result of the C++ binding, which is a status where the call was refused or failed."""
+    if type(result) is int:
+        _check(result, what)
+    return result
 
-    __slots__ = ("index", "ctx")
 
-    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
-        self.index, self.ctx = index, None
-        if stream is not None:
-            if stream.device.index != index:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
-            self.ctx = torch.cuda.stream(stream)
-        elif index != torch._C._cuda_getDevice():
-            self.ctx = torch.cuda.device(index)
-
-    def __enter__(self) -> int:
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc) -> None:
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on_stream(stream: torch.cuda.Stream, tensor: torch.Tensor):
+    """`stream` as torch's current one, so that outputs and workspaces belong to it."""
+    if tensor.device != stream.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {tensor.device}")
+    return torch.cuda.stream(stream)
 
 
 def rotary(q: torch.Tensor, k: Optional[torch.Tensor], heads: int, kv_heads: int, inv_freq: torch.Tensor,
@@ -526,49 +503,12 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], heads: int, kv_heads: int
     positions: int32 or int64, [b, s] or [s], or None: token t is at offset +
     t. inverse=True is the gradient: dq, dk of the turned q, k in, of q, k out.
     q_out and k_out may be q and k themselves. Returns (q_out, k_out)."""
-    if q.dim() != 3:
-        raise ValueError("q must be [b, s, heads * dh]")
-    b, s, width = q.shape
-    if heads <= 0 or width % heads:
-        raise ValueError(f"q's last dimension {width} does not hold {heads} heads")
-    dh = width // heads
-    kinds = (torch.bfloat16, torch.float32)
-    pq = _rows(q, "q", heads * dh, kinds)
-    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise TypeError("inv_freq must be a contiguous fp64 vector in host memory")
-    pk = (None, 0, 0)
-    if k is None:
-        kv_heads, k_out = 0, None
-    else:
-        pk = _rows(k, "k", kv_heads * dh, kinds, q)
-    at, size, step = None, 8, 0
-    if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64) or positions.get_device() != q.get_device():
-            raise TypeError("positions must be int32 or int64 on q's device")
-        shape, stride = positions.shape, positions.stride()
-        if shape != (b, s) and shape != (s,):
-            raise ValueError(f"positions has shape {tuple(shape)}, expected {(b, s)} or {(s,)}")
-        if stride[-1] != 1 and s > 1:
-            raise ValueError("positions must be contiguous along the sequence")
-        at, size = positions.data_ptr(), positions.element_size()
-        step = stride[0] if len(shape) == 2 else 0
-    dtype = BPT_DTYPE_F32 if q.dtype == torch.float32 else BPT_DTYPE_BF16
-    with _On(q.get_device(), stream) as st:
-        if q_out is None:
-            q_out, pqo = _new_rows(q, b, s, heads * dh)
-        else:
-            pqo = _rows(q_out, "q_out", heads * dh, kinds, q)
-        if k is None:
-            pko = (None, 0, 0)
-        elif k_out is None:
-            k_out, pko = _new_rows(k, b, s, kv_heads * dh)
-        else:
-            pko = _rows(k_out, "k_out", kv_heads * dh, kinds, q)
-        r = lib().bpt_rotary(dtype, *pq, *pk, b, s, heads, kv_heads, dh, 2 * inv_freq.numel(), int(bool(interleaved)),
-                             inv_freq.data_ptr(), float(magnitude), at, size, step, int(offset), int(bool(inverse)),
-                             *pqo, *pko, st)
-    _check(r, "bpt_rotary")
-    return q_out, k_out
+    if stream is not None:
+        with _on_stream(stream, q):
+            return rotary(q, k, heads, kv_heads, inv_freq, positions, offset, interleaved, magnitude, inverse, q_out,
+                          k_out)
+    return _done((_fast or _load_binding()).rotary(q, k, heads, kv_heads, inv_freq, positions, offset, interleaved, magnitude,
+                                              inverse, q_out, k_out), "bpt_rotary")
 
 
 class KV4Cache:
@@ -584,26 +524,11 @@ class KV4Cache:
             raise ValueError("dh must be 64 or 128")
         if data.dtype != torch.uint8 or not data.is_cuda or not data.is_contiguous():
             raise TypeError("data must be a contiguous uint8 CUDA tensor")
-        if data.dim() != 4 or data.shape[3] != block:
-            raise ValueError(f"data has shape {tuple(data.shape)}, expected [b, kv_heads, capacity / 64, {block}]")
+        shape = data.shape
+        if len(shape) != 4 or shape[3] != block:
+            raise ValueError(f"data has shape {tuple(shape)}, expected [b, kv_heads, capacity / 64, {block}]")
         self.data, self.dh = data, dh
-        self.b, self.kv_heads, self.capacity = data.shape[0], data.shape[1], data.shape[2] * 64
-
-    def _args(self) -> tuple:
-        return self.data.data_ptr(), self.b, self.kv_heads, self.capacity, self.dh
-
-    def _ints(self, t: torch.Tensor, name: str) -> int:
-        if t.dtype != torch.int32 or t.device != self.data.device or tuple(t.shape) != (self.b,) \
-                or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor [{self.b}] on the cache's device")
-        return t.data_ptr()
-
-    def _floats(self, t: torch.Tensor, name: str) -> int:
-        shape = (self.b, self.kv_heads, self.capacity)
-        if t.dtype != torch.float32 or t.device != self.data.device or tuple(t.shape) != shape \
-                or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous fp32 tensor {shape} on the cache's device")
-        return t.data_ptr()
+        self.b, self.kv_heads, self.capacity = shape[0], shape[1], shape[2] * 64
 
 
 def kv4_cache(b: int, kv_heads: int, capacity: int, dh: int, device="cuda") -> KV4Cache:
@@ -622,16 +547,10 @@ def kv4_store(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, start: torch.Te
     """Store tokens (bf16 [b, n, kv_heads * dh], rows contiguous) at places
     start[beta] .. of each sequence, the first counts[beta] of them (default:
     all n); start and counts int32 [b] (bpt_kv4_store)."""
-    width = cache.kv_heads * cache.dh
-    pk = _rows(k, "k", width, (torch.bfloat16,))
-    pv = _rows(v, "v", width, (torch.bfloat16,), k)
-    if k.shape[0] != cache.b or k.device != cache.data.device:
-        raise ValueError(f"k must hold {cache.b} sequences on the cache's device")
-    ps = cache._ints(start, "start")
-    pc = None if counts is None else cache._ints(counts, "counts")
-    with _On(k.get_device(), stream) as st:
-        r = lib().bpt_kv4_store(*cache._args(), *pk, *pv, k.shape[1], ps, pc, st)
-    _check(r, "bpt_kv4_store")
+    if stream is not None:
+        with _on_stream(stream, cache.data):
+            return kv4_store(cache, k, v, start, counts)
+    _done((_fast or _load_binding()).kv4_store(cache.data, cache.dh, k, v, start, counts), "bpt_kv4_store")
 
 
 def kv4_load(cache: KV4Cache, lens: torch.Tensor, n: int, start: Optional[torch.Tensor] = None,
@@ -639,20 +558,10 @@ def kv4_load(cache: KV4Cache, lens: torch.Tensor, n: int, start: Optional[torch.
     """The values at places start[beta] .. start[beta] + n - 1 (default: from 0)
     of each sequence, as bf16 k, v [b, n, kv_heads * dh]; zeros at or past
     lens[beta] (bpt_kv4_load)."""
-    pl = cache._ints(lens, "lens")
-    ps = None if start is None else cache._ints(start, "start")
-    dev = cache.data.device
-    with _On(dev.index, stream) as st:
-        k = torch.empty(cache.b, n, cache.kv_heads * cache.dh, dtype=torch.bfloat16, device=dev)
-        v = torch.empty_like(k)
-        r = lib().bpt_kv4_load(*cache._args(), ps, pl, n, k.data_ptr(), v.data_ptr(), st)
-    _check(r, "bpt_kv4_load")
-    return k, v
-
-
-@functools.lru_cache(maxsize=256)
-def _kv4_workspace_bytes(b: int, n: int, heads: int, kv_heads: int, capacity: int, dh: int, weights: bool) -> int:
-    return int(lib().bpt_kv4_attention_workspace_bytes(b, n, heads, kv_heads, capacity, dh, int(weights)))
+    if stream is not None:
+        with _on_stream(stream, cache.data):
+            return kv4_load(cache, lens, n, start)
+    return _done((_fast or _load_binding()).kv4_load(cache.data, cache.dh, lens, n, start), "bpt_kv4_load")
 
 
 def kv4_attention(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, heads: int, causal: bool = True,
@@ -663,23 +572,11 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, heads: i
     among them (bpt_kv4_attention). weights: fp32 [b, kv_heads, capacity], to
     which every cached token's softmax weight is added. Returns o (bf16 [b, n,
     heads * dh]), with return_lse (o, lse2 fp32 [b, heads, n])."""
-    pq = _rows(q, "q", heads * cache.dh, (torch.bfloat16,))
-    if q.shape[0] != cache.b or q.device != cache.data.device:
-        raise ValueError(f"q must hold {cache.b} sequences on the cache's device")
-    pl = cache._ints(lens, "lens")
-    pw = None if weights is None else cache._floats(weights, "weights")
-    n, dev = q.shape[1], q.device
-    data, b, kv_heads, capacity, dh = cache._args()
-    nbytes = _kv4_workspace_bytes(b, n, heads, kv_heads, capacity, dh, pw is not None)
-    with _On(dev.index, stream) as st:
-        o = _new_rows(q, b, n, heads * dh)[0]
-        lse2 = torch.empty(b, heads, n, dtype=torch.float32, device=dev) if return_lse else None
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        r = lib().bpt_kv4_attention(*pq, data, pl, b, n, heads, kv_heads, capacity, dh, int(bool(causal)),
-                                    o.data_ptr(), None if lse2 is None else lse2.data_ptr(), pw,
-                                    ws.data_ptr() if nbytes else None, nbytes, st)
-    _check(r, "bpt_kv4_attention")
-    return (o, lse2) if return_lse else o
+    if stream is not None:
+        with _on_stream(stream, q):
+            return kv4_attention(q, cache, lens, heads, causal, weights, return_lse)
+    return _done((_fast or _load_binding()).kv4_attention(q, cache.data, cache.dh, lens, heads, causal, weights, return_lse),
+                 "bpt_kv4_attention")
 
 
 def kv4_evict(cache: KV4Cache, weights: torch.Tensor, lens: torch.Tensor, keep: int, recent: int, out: KV4Cache,
@@ -688,19 +585,11 @@ def kv4_evict(cache: KV4Cache, weights: torch.Tensor, lens: torch.Tensor, keep: 
     to the cache `out` (bpt_kv4_evict). weights: fp32 [b, kv_heads, capacity]
     as kv4_attention accumulates them. Returns (kept int32 [b, kv_heads, keep],
     -1 past the kept ones; the new lens; the kept tokens' weights, for out)."""
-    dev = cache.data.device
-    if (out.b, out.kv_heads, out.dh) != (cache.b, cache.kv_heads, cache.dh) or out.data.device != dev:
-        raise ValueError("out must have the sequences, heads and device of the cache")
-    pw, pl = cache._floats(weights, "weights"), cache._ints(lens, "lens")
-    data, b, kv_heads, capacity, dh = cache._args()
-    with _On(dev.index, stream) as st:
-        kept = torch.empty(b, kv_heads, max(int(keep), 0), dtype=torch.int32, device=dev)
-        new_lens = torch.empty_like(lens)
-        new_weights = torch.empty(b, kv_heads, out.capacity, dtype=torch.float32, device=dev)
-        r = lib().bpt_kv4_evict(data, pw, pl, b, kv_heads, capacity, dh, int(keep), int(recent), out.data.data_ptr(),
-                                out.capacity, new_weights.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), st)
-    _check(r, "bpt_kv4_evict")
-    return kept, new_lens, new_weights
+    if stream is not None:
+        with _on_stream(stream, cache.data):
+            return kv4_evict(cache, weights, lens, keep, recent, out)
+    return _done((_fast or _load_binding()).kv4_evict(cache.data, cache.dh, weights, lens, keep, recent, out.data, out.dh),
+                 "bpt_kv4_evict")
 
 
 def stream_status(stream: Optional[torch.cuda.Stream] = None) -> int:

@@ -1,4 +1,5 @@
-"""Build the CUDA library libbpt.so in-tree for sm_100a.
+"""Build the CUDA library libbpt.so in-tree for sm_100a, and the part of the
+Python binding that is C++ (csrc/binding.cpp, linked with it).
 
     python -m blockwise_attn_ffn_bpt_b200.build [--force] [--verbose]
 
@@ -15,12 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbpt.so")
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -44,10 +47,37 @@ def sources():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in sources())
+    return _newer(LIB, sources()) and _newer(BINDING, binding_sources())
+
+
+def binding_sources():
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "bpt.h")]
+
+
+def _newer(built: str, sources) -> bool:
+    return os.path.exists(built) and all(os.path.getmtime(p) <= os.path.getmtime(built) for p in sources)
+
+
+def build_binding() -> str:
+    """The g++ on PATH, as nvcc takes for the library (a compiler that links its own static libstdc++ would put a
+    second one, with locales of its own, beside torch's), against the installed torch; finds libbpt.so beside itself."""
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *[f"-isystem{p}" for p in include], "-o", tmp,
+           os.path.join(CSRC, "binding.cpp"), "-L", PKG, "-l:libbpt.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stdout + res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -65,6 +95,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         f.write(" ".join(cmd) + "\n" + log)
     if verbose:
         print(log)
+    build_binding()
     return LIB
 
 

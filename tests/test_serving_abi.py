@@ -170,3 +170,15 @@ def test_the_binding_refuses_host_tensors():
         bpt.KV4Cache(torch.zeros(1, 1, 1, 9216, dtype=torch.uint8), 96)
     with pytest.raises(ValueError):
         bpt.kv4_cache(1, 1, 64, 96, device="cpu")
+
+
+def test_the_binding_refuses_before_it_touches_a_gpu():
+    # messages with numbers in them, raised from C++
+    freq, _ = bpt.rotary_frequencies(64)
+    q = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q's last dimension 128 does not hold 3 heads"):
+        bpt.rotary(q, None, 3, 0, freq)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        bpt.rotary(q, None, 2, 0, freq)
+    with pytest.raises(ValueError, match="heads = 4294967296 is out of range"):
+        bpt.rotary(q, None, 1 << 32, 0, freq)
