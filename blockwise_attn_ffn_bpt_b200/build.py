@@ -72,7 +72,7 @@ def build_binding() -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            *[f"-isystem{p}" for p in include], "-o", tmp,
            os.path.join(CSRC, "binding.cpp"), "-L", PKG, "-l:libbpt.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10",
-           "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", f"-Wl,-rpath,{lib}"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stdout + res.stderr}")

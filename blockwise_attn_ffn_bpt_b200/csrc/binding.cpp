@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -74,7 +75,7 @@ int count_of(int64_t n, const char* name) {
 }
 
 at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor& like) {
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(like.device()));
+  return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);  // at::empty without the dispatcher
 }
 
 Rows new_rows(const at::Tensor& t) { return Rows{t.data_ptr(), t.stride(0), t.stride(1)}; }
