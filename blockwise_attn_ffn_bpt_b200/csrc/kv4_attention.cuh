@@ -216,13 +216,14 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem + warp * C::STAGES * L::BYTES;
   const uint32_t bars = smem + C::RING + warp * C::STAGES * 8;
-  grid_dependents_start();
   if (threadIdx.x == 0) *flag = 0;
   if (lane == 0)
     for (int i = 0; i < C::STAGES; ++i) mbar_init(bars + i * 8, 1);
   fence_mbar_init();
   __syncthreads();
   const Abort ab{flag, a.status};
+  grid_dependency_wait();
+  grid_dependents_start();  // not earlier: the kernels behind read lens and the weights before they wait
 
   const int rows = a.d.kv_heads * a.blocks_of_cols, group = a.heads / a.d.kv_heads;
   if (blockIdx.x == 0 && warp == 0)
@@ -832,6 +833,7 @@ __global__ void __launch_bounds__(KVW_THREADS, 8) kv4_weights_kernel(const __gri
       if (key + v * STEP < a.d.capacity) old[v] = *reinterpret_cast<const float4*>(to + key + v * STEP);
     const int len = min(max(a.lens[beta], 0), a.d.capacity);
     grid_dependency_wait();
+    grid_dependents_start();
     if (key >= len) continue;
     const float* s = a.scores + (long long)row * cols * a.d.capacity + key;
     const float* lse2 = a.lse2 + ((long long)beta * a.heads + kvh * group) * a.n;

@@ -146,6 +146,8 @@ template <int DH, bool WIDE>
 __global__ void __launch_bounds__(KV4_THREADS) kv4_store_kernel(const __grid_constant__ Kv4StoreArgs a) {
   constexpr int U = DH / 16;
   using L = Kv4<DH>;
+  grid_dependency_wait();
+  grid_dependents_start();
   const unsigned i = blockIdx.x * (unsigned)KV4_THREADS + threadIdx.x;
   const int u = i % U;
   const unsigned rest = i / U;
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_store_kernel(const __grid_con
         if (WIDE) {
           load_stream32(src, raw[w]);
         } else {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src)), y = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+          const uint4 x = reinterpret_cast<const uint4*>(src)[0], y = reinterpret_cast<const uint4*>(src)[1];
           raw[w][0] = x.x, raw[w][1] = x.y, raw[w][2] = x.z, raw[w][3] = x.w;
           raw[w][4] = y.x, raw[w][5] = y.y, raw[w][6] = y.z, raw[w][7] = y.w;
         }
@@ -241,6 +243,8 @@ template <int DH, bool WIDE>
 __global__ void __launch_bounds__(KV4_THREADS) kv4_load_kernel(const __grid_constant__ Kv4LoadArgs a) {
   constexpr int U = DH / 16;
   using L = Kv4<DH>;
+  grid_dependency_wait();
+  grid_dependents_start();
   const unsigned i = blockIdx.x * (unsigned)KV4_THREADS + threadIdx.x;
   const int u = i % U;
   const unsigned rest = i / U;
@@ -259,9 +263,9 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_load_kernel(const __grid_cons
       uint32_t word[2][2], params[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        word[0][w] = __ldg(reinterpret_cast<const uint32_t*>(block + r * L::ROW) + kv4_k_place<DH>(2 * u + w));
-        word[1][w] = __ldg(reinterpret_cast<const uint32_t*>(block + L::V_CODES + r * L::ROW) + kv4_v_place<DH>(2 * u + w, r));
-        params[w] = __ldg(reinterpret_cast<const uint32_t*>(block + (w ? L::V_PARAMS : L::K_PARAMS) + r * L::PROW) + u / 4);
+        word[0][w] = reinterpret_cast<const uint32_t*>(block + r * L::ROW)[kv4_k_place<DH>(2 * u + w)];
+        word[1][w] = reinterpret_cast<const uint32_t*>(block + L::V_CODES + r * L::ROW)[kv4_v_place<DH>(2 * u + w, r)];
+        params[w] = reinterpret_cast<const uint32_t*>(block + (w ? L::V_PARAMS : L::K_PARAMS) + r * L::PROW)[u / 4];
       }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {

@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = CL > 1 ? (int)cluster_ctarank() : 0;
   const int rows = a.d.b * a.d.kv_heads;
+  grid_dependency_wait();
   grid_dependents_start();
   for (int row = blockIdx.x / CL; row < rows; row += gridDim.x / CL) {
     const int beta = row / a.d.kv_heads;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
     const int quads = min(share, every - quad0);
     auto keys_of = [&](int i, bool read) -> uint4 {
       if (CACHED && !read) return cached[i];
-      const uint4 k = weight_keys(__ldg(reinterpret_cast<const float4*>(w) + quad0 + i), 4 * (quad0 + i), old);
+      const uint4 k = weight_keys(reinterpret_cast<const float4*>(w)[quad0 + i], 4 * (quad0 + i), old);
       if (CACHED) cached[i] = k;
       return k;
     };
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_move_kernel(const __grid_cons
   const int j0 = blockIdx.x * (TEAMS * MOVE_ROWS) + threadIdx.x / TEAM;
   const int rows = a.d.b * a.d.kv_heads;
   grid_dependency_wait();
+  grid_dependents_start();
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     const int left = a.lens_out[row / a.d.kv_heads];
     const uint8_t* src = a.src + (long long)row * a.d.blocks() * L::BYTES;
@@ -320,13 +322,13 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_move_kernel(const __grid_cons
       const int r = from[k] % KV4_BLOCK;
       const uint8_t* block = src + (long long)(from[k] / KV4_BLOCK) * L::BYTES;
       const int at = (piece < C ? 0 : L::V_CODES) + r * L::ROW + (piece < C ? piece : piece - C) * 16;
-      codes[k] = __ldg(reinterpret_cast<const uint4*>(block + at));
+      codes[k] = *reinterpret_cast<const uint4*>(block + at);
       if (piece < 2) {
 #pragma unroll
         for (int g = 0; g < L::GROUPS; ++g)
-          params[k][g] = __ldg(reinterpret_cast<const uint32_t*>(block + (piece == 0 ? L::K_PARAMS : L::V_PARAMS) + r * L::PROW) + g);
+          params[k][g] = reinterpret_cast<const uint32_t*>(block + (piece == 0 ? L::K_PARAMS : L::V_PARAMS) + r * L::PROW)[g];
       }
-      if (piece == 2) weight[k] = __ldg(a.weights + (long long)row * a.d.capacity + from[k]);
+      if (piece == 2) weight[k] = a.weights[(long long)row * a.d.capacity + from[k]];
     }
 #pragma unroll
     for (int k = 0; k < MOVE_ROWS; ++k) {

@@ -138,8 +138,10 @@ __device__ __forceinline__ bool counter_wait(const unsigned* cnt, unsigned targe
 // ---------------------------------------------------------------- dependent launches
 // A kernel launched with programmatic stream serialization starts once every
 // block of the one before it has called grid_dependents_start (or ended), and
-// must not touch what that one writes before grid_dependency_wait, which waits
-// for its end.
+// must not touch what that one reads or writes before grid_dependency_wait, which
+// waits for its end. A kernel that calls grid_dependents_start after that keeps
+// the earlier ones out of reach of the next one altogether. What is read may have
+// been written during this kernel, so by plain loads, not read-only ones.
 __device__ __forceinline__ void grid_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

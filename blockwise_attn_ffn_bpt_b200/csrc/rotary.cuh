@@ -80,6 +80,8 @@ __device__ __forceinline__ int rot_place(int j, int pairs) {
 template <typename T, int W, bool INTERLEAVED>
 __global__ void __launch_bounds__(ROT_THREADS, ROT_BLOCKS) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   __shared__ alignas(16) float2 table[ROT_TABLE];
+  grid_dependency_wait();
+  grid_dependents_start();
   const int tok0 = blockIdx.x * a.tile;
   const int ntok = min(a.tile, a.tokens - tok0);
   const int beta0 = tok0 / a.s, first = tok0 - beta0 * a.s;

@@ -85,48 +85,37 @@ int check_kv4(int b, int n, int kv_heads, int capacity, int dh) {
   return BPT_OK;
 }
 
-// Launches a kernel that may start before the one ahead of it on the stream has
-// ended (it waits for that itself: grid_dependency_wait).
+// Launches a kernel, in clusters of `cl` blocks where cl > 1, that may start
+// before the one ahead of it on the stream has ended: it waits for that itself
+// (grid_dependency_wait), with its launch behind it. What follows it may start
+// so too, whatever it is, because every kernel launched here waits in all its
+// blocks: its end is also the end of all before it.
 template <typename Args>
-int launch_dependent(void (*kernel)(const Args), const Args& args, dim3 grid, unsigned threads, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
-}
-
-// Launches a kernel in clusters of `cl` blocks.
-template <typename Args>
-int launch_cluster(void (*kernel)(const Args), const Args& args, dim3 grid, unsigned threads, int cl, size_t smem,
-                   cudaStream_t st) {
+int launch_kernel(void (*kernel)(const Args), const Args& args, dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                  int cl = 1) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)cl;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cl;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cl > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess) return BPT_OK;
+  cudaGetLastError();
+  return BPT_ERR_CUDA;
 }
 
 unsigned grid_y(long long rows) { return (unsigned)std::min<long long>(rows, 65535); }
 
 template <typename T, int W>
-void launch_rotary(const RotaryArgs& a, bool interleaved, dim3 grid, cudaStream_t st) {
-  if (interleaved)
-    rotary_kernel<T, W, true><<<grid, ROT_THREADS, 0, st>>>(a);
-  else
-    rotary_kernel<T, W, false><<<grid, ROT_THREADS, 0, st>>>(a);
+int launch_rotary(const RotaryArgs& a, bool interleaved, dim3 grid, cudaStream_t st) {
+  return launch_kernel(interleaved ? rotary_kernel<T, W, true> : rotary_kernel<T, W, false>, a, grid, ROT_THREADS, 0, st);
 }
 
 struct Kv4AttnLayout {
@@ -279,15 +268,15 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
   {
     LaunchScope ls("rotary", st);
     if (es == 2 && w == 8)
-      launch_rotary<__nv_bfloat16, 8>(a, interleaved, grid, st);
+      BPT_TRY((launch_rotary<__nv_bfloat16, 8>(a, interleaved, grid, st)));
     else if (es == 2)
-      launch_rotary<__nv_bfloat16, 1>(a, interleaved, grid, st);
+      BPT_TRY((launch_rotary<__nv_bfloat16, 1>(a, interleaved, grid, st)));
     else if (w == 4)
-      launch_rotary<float, 4>(a, interleaved, grid, st);
+      BPT_TRY((launch_rotary<float, 4>(a, interleaved, grid, st)));
     else
-      launch_rotary<float, 1>(a, interleaved, grid, st);
+      BPT_TRY((launch_rotary<float, 1>(a, interleaved, grid, st)));
   }
-  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  return BPT_OK;
 }
 
 size_t bpt_kv4_cache_bytes(int b, int kv_heads, int capacity, int dh) {
@@ -331,9 +320,9 @@ int bpt_kv4_store(void* cache, int b, int kv_heads, int capacity, int dh, const 
     LaunchScope ls("kv4_store", st);
     auto kernel = dh == 128 ? (wide ? kv4_store_kernel<128, true> : kv4_store_kernel<128, false>)
                             : (wide ? kv4_store_kernel<64, true> : kv4_store_kernel<64, false>);
-    kernel<<<grid, KV4_THREADS, 0, st>>>(a);
+    BPT_TRY(launch_kernel(kernel, a, grid, KV4_THREADS, 0, st));
   }
-  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  return BPT_OK;
 }
 
 int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, const int* start, const int* lens,
@@ -368,9 +357,9 @@ int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, c
     LaunchScope ls("kv4_load", st);
     auto kernel = dh == 128 ? (wide ? kv4_load_kernel<128, true> : kv4_load_kernel<128, false>)
                             : (wide ? kv4_load_kernel<64, true> : kv4_load_kernel<64, false>);
-    kernel<<<grid, KV4_THREADS, 0, st>>>(a);
+    BPT_TRY(launch_kernel(kernel, a, grid, KV4_THREADS, 0, st));
   }
-  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  return BPT_OK;
 }
 
 size_t bpt_kv4_attention_workspace_bytes(int b, int n, int heads, int kv_heads, int capacity, int dh,
@@ -431,21 +420,21 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   {
     LaunchScope ls("kv4_attention", st);
     const unsigned grid = L.direct ? (unsigned)L.segments : (unsigned)std::min(most, (a.max_warps + L.warps - 1) / L.warps);
-    kva_kernel(dh, L.cols, L.direct)<<<grid, L.warps * 32, kva_smem(dh, L.cols), st>>>(a);
+    BPT_TRY(launch_kernel(kva_kernel(dh, L.cols, L.direct), a, grid, L.warps * 32, kva_smem(dh, L.cols), st));
   }
   if (!L.direct) {
     LaunchScope ls("kv4_join", st);
     const dim3 grid((unsigned)(kv_heads * L.cols), grid_y(b));
-    BPT_TRY(launch_dependent(dh == 128 ? kv4_join_kernel<128> : kv4_join_kernel<64>, a, grid, KVJ_WARPS * 32, st));
+    BPT_TRY(launch_kernel(dh == 128 ? kv4_join_kernel<128> : kv4_join_kernel<64>, a, grid, KVJ_WARPS * 32, 0, st));
   }
   if (weights) {
     LaunchScope ls("kv4_weights", st);
     const Kv4WeightsArgs w{a.scores, a.lse2, weights, a.d, lens, n, heads, a.causal};
     const int per = KVW_THREADS * 4 * KVW_VECTORS;
     const dim3 grid((unsigned)((capacity + per - 1) / per), grid_y((long long)b * kv_heads));
-    BPT_TRY(launch_dependent(kv4_weights_kernel, w, grid, KVW_THREADS, st));
+    BPT_TRY(launch_kernel(kv4_weights_kernel, w, grid, KVW_THREADS, 0, st));
   }
-  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  return BPT_OK;
 }
 
 int bpt_kv4_evict(const void* cache, const float* weights, const int* lens, int b, int kv_heads, int capacity,
@@ -486,8 +475,8 @@ int bpt_kv4_evict(const void* cache, const float* weights, const int* lens, int 
     const int cl = evict_cluster((long long)rows, capacity);
     const size_t share = (size_t)(capacity / 4 + cl - 1) / cl * 4;  // tokens of a block
     const bool cached = share <= EVICT_CACHED;
-    BPT_TRY(launch_cluster(evict_kernel(cl, cached), a, dim3((unsigned)rows * cl), EVICT_THREADS, cl,
-                           cached ? share * 4 : 0, st));
+    BPT_TRY(launch_kernel(evict_kernel(cl, cached), a, dim3((unsigned)rows * cl), EVICT_THREADS, cached ? share * 4 : 0, st,
+                          cl));
   }
   {
     LaunchScope ls("kv4_move", st);
@@ -495,9 +484,9 @@ int bpt_kv4_evict(const void* cache, const float* weights, const int* lens, int 
                         weights, weights_out, kept, lens_out, keep};
     const int per = KV4_THREADS / (dh == 128 ? 8 : 4) * MOVE_ROWS;
     const dim3 grid((unsigned)((capacity_out + per - 1) / per), grid_y((long long)rows));
-    BPT_TRY(launch_dependent(dh == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>, a, grid, KV4_THREADS, st));
+    BPT_TRY(launch_kernel(dh == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>, a, grid, KV4_THREADS, 0, st));
   }
-  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ERR_CUDA;
+  return BPT_OK;
 }
 
 }  // extern "C"

@@ -393,6 +393,87 @@ def test_a_captured_step_and_eviction(capacity):
     assert bpt.stream_status() == 0
 
 
+@pytest.mark.parametrize("heads,kv,dh,start", [(4, 2, 64, 300), (16, 8, 128, 9000)])
+def test_calls_that_follow_closely_wait_for_each_other(heads, kv, dh, start):
+    # each call reads what the one ahead writes, or writes what that one reads, with nothing between them; the same
+    # calls with the device idle before each give the same bits
+    b, steps, keep, width = 4, 12, 128, kv * dh
+    capacity = start + 100
+    base, _ = filled(b, kv, dh, [start - 11 * i for i in range(b)], capacity, seed=61)
+    rows = bf16((b, 1, heads * dh + 2 * width), 62)
+    freq, _ = bpt.rotary_frequencies(dh)
+
+    def run(between):
+        cache, small = bpt.KV4Cache(base.data.clone(), dh), bpt.kv4_cache(b, kv, keep, dh)
+        lens = ints(*[start - 11 * i for i in range(b)])
+        at = [lens + i for i in range(steps + 1)]
+        w = torch.zeros((b, kv, cache.capacity), device="cuda")
+        q, k, v = rows[..., :heads * dh].clone(), rows[..., heads * dh:-width].clone(), rows[..., -width:].clone()
+        out = []
+        for i in range(steps):
+            between()
+            bpt.rotary(q, k, heads, kv, freq, positions=at[i].view(b, 1), q_out=q, k_out=k)
+            between()
+            bpt.kv4_store(cache, k, v, at[i])
+            between()
+            out.append(bpt.kv4_attention(q, cache, at[i + 1], heads, weights=w))
+            between()
+            out.extend(bpt.kv4_evict(cache, w, at[i + 1], keep, 7, small))  # reads the weights, rewrites `small`
+            between()
+            out.extend(bpt.kv4_load(small, out[-2], keep))
+            between()
+            out.append(bpt.kv4_attention(q, small, out[-4], heads, weights=out[-3]))
+            between()
+            bpt.kv4_store(small, k, v, ints_zero)  # rewrites what the attention ahead reads
+        return [*out, q, k, w, cache.data, small.data]
+
+    ints_zero = ints(*[0] * b)
+    ref = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for x, y in zip(run(lambda: None), ref, strict=True):
+            assert torch.equal(x, y)
+    assert bpt.stream_status() == 0
+
+
+def test_captured_behind_copies_fills_and_other_streams():
+    # what a captured call follows is a copy, a fill, a kernel of torch's and another stream's call
+    lens, capacity = [500, 333], 512
+    base, _ = filled(2, 2, 64, lens, capacity, seed=71)
+    x, y = bf16((2, 1, 4 * 64), 72), torch.empty((2, 1, 4 * 64), dtype=torch.bfloat16, device="cuda")
+    kv = bf16((2, 1, 2 * 64), 73)
+    n, freq = ints(*lens), bpt.rotary_frequencies(64)[0]
+    w = torch.zeros((2, 2, capacity), device="cuda")
+    cache = bpt.KV4Cache(base.data.clone(), 64)
+    side = torch.cuda.Stream()
+
+    def step():
+        cache.data.copy_(base.data)
+        bpt.kv4_store(cache, kv, kv, n)
+        y.copy_(x)
+        bpt.rotary(y, None, 4, 0, freq, offset=5, q_out=y)
+        w.zero_()
+        o = bpt.kv4_attention(y, cache, n, 4, weights=w)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            k, v = bpt.kv4_load(cache, n, 500)
+        bpt.rotary(y, None, 4, 0, freq, offset=6, q_out=y)
+        torch.cuda.current_stream().wait_stream(side)
+        bpt.kv4_store(cache, kv, kv, n - 1)
+        return o, k, v, bpt.kv4_attention(y, cache, n, 4, weights=w)
+
+    ref = [t.clone() for t in step()] + [w.clone(), y.clone(), cache.data.clone()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, e in zip((*out, w, y, cache.data), ref, strict=True):
+            assert torch.equal(a, e)
+    assert bpt.stream_status() == 0
+
+
 def test_two_streams_at_once():
     lens = [1000, 400]
     cache, _ = filled(2, 4, 64, lens, 1024, seed=17)
