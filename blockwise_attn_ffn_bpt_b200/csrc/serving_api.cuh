@@ -217,11 +217,12 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
   const TokenRows pos{positions, b, s, position_stride * position_bytes, position_bytes, (size_t)position_bytes};
   if (positions && (!strides_ok(pos) || reinterpret_cast<uintptr_t>(positions) % position_bytes))
     return strides_ok(pos) ? BPT_ERR_ALIGN : BPT_ERR_SHAPE;
-  bool wide = true, in_place[2] = {false, false};
+  int w = 16 / es;  // elements of a vector: 16 bytes, or fewer as the rows are aligned
+  bool in_place[2] = {false, false};
   for (int i = 0; i < nt; ++i) {
     if (!strides_ok(in[i]) || !strides_ok(out[i]) || !rows_distinct(out[i])) return BPT_ERR_SHAPE;
     if (!aligned(in[i], es) || !aligned(out[i], es)) return BPT_ERR_ALIGN;
-    wide = wide && aligned(in[i], 16) && aligned(out[i], 16);
+    while (w > 1 && !(aligned(in[i], w * es) && aligned(out[i], w * es))) w /= 2;
     in_place[i] = same_rows(in[i], out[i]);
   }
   for (int i = 0; i < nt; ++i) {
@@ -231,10 +232,8 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
   }
   if (keys && rows_overlap(out[0], out[1])) return BPT_ERR_ALIAS;
 
-  // 16-byte vectors where a vector holds whole pairs' halves of every row;
-  // one pair at a time otherwise
-  const int full = 16 / es;
-  const int w = wide && (rot / 2) % full == 0 ? full : 1;
+  // the turned part of a head is whole vectors of its pairs' halves
+  while ((rot / 2) % w) w /= 2;
   RotaryArgs a{};
   for (int i = 0; i < nt; ++i)
     a.t[i] = {in[i].p, const_cast<void*>(out[i].p), in[i].bs / es, in[i].ld / es, out[i].bs / es, out[i].ld / es};
@@ -265,18 +264,15 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
   BPT_TRY(check_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)(((long long)a.tokens + a.tile - 1) / a.tile), (a.units + a.chunk - 1) / a.chunk);
-  {
-    LaunchScope ls("rotary", st);
-    if (es == 2 && w == 8)
-      BPT_TRY((launch_rotary<__nv_bfloat16, 8>(a, interleaved, grid, st)));
-    else if (es == 2)
-      BPT_TRY((launch_rotary<__nv_bfloat16, 1>(a, interleaved, grid, st)));
-    else if (w == 4)
-      BPT_TRY((launch_rotary<float, 4>(a, interleaved, grid, st)));
-    else
-      BPT_TRY((launch_rotary<float, 1>(a, interleaved, grid, st)));
-  }
-  return BPT_OK;
+  LaunchScope ls("rotary", st);
+  if (es == 4)
+    return w == 4   ? launch_rotary<float, 4>(a, interleaved, grid, st)
+           : w == 2 ? launch_rotary<float, 2>(a, interleaved, grid, st)
+                    : launch_rotary<float, 1>(a, interleaved, grid, st);
+  return w == 8   ? launch_rotary<__nv_bfloat16, 8>(a, interleaved, grid, st)
+         : w == 4 ? launch_rotary<__nv_bfloat16, 4>(a, interleaved, grid, st)
+         : w == 2 ? launch_rotary<__nv_bfloat16, 2>(a, interleaved, grid, st)
+                  : launch_rotary<__nv_bfloat16, 1>(a, interleaved, grid, st);
 }
 
 size_t bpt_kv4_cache_bytes(int b, int kv_heads, int capacity, int dh) {

@@ -49,6 +49,7 @@ def check(got, x, positions, freq, heads, magnitude, interleaved, inverse):
 @pytest.mark.parametrize("b,s,heads,kv,dh,rot", [
     (1, 1, 1, 1, 64, 64), (3, 1, 32, 4, 128, 128), (2, 37, 5, 1, 64, 32), (1, 129, 4, 2, 128, 24),
     (2, 5, 80, 40, 128, 2), (1, 1000, 3, 3, 64, 48),
+    (2, 700, 3, 1, 128, 20), (1, 300, 2, 2, 64, 56), (1, 33, 2, 1, 64, 6),
 ])
 def test_against_the_oracle(b, s, heads, kv, dh, rot, interleaved, dtype):
     q, k = rand((b, s, heads * dh), dtype, 1), rand((b, s, kv * dh), dtype, 2)
@@ -81,11 +82,11 @@ def test_positions_of_their_own_far_away_and_scaled(dtype):
     check(qo, q, pos.numpy(), freq, heads, m, False, False)
 
 
-@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("shift", [0, 1, 2, 4])
 @pytest.mark.parametrize("layout", ["sequences", "tokens"])
 def test_strided_rows_in_place_leave_their_neighbours(layout, shift):
-    # q and k as columns of one fused buffer, turned in place; shifted by one
-    # element the rows are not 16-byte aligned
+    # q and k as columns of one fused buffer, turned in place; shifted by 1, 2
+    # or 4 elements the rows are aligned to 2, 4 or 8 bytes
     b, s, heads, kv, dh = 2, 9, 3, 1, 64
     wide = (heads + 2 * kv) * dh + 8
     x = rand((b, s, wide) if layout == "sequences" else (s, b, wide), torch.bfloat16, 4)
