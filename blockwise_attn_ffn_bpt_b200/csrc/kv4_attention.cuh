@@ -713,31 +713,40 @@ inline bool kva_set_attributes() {
   return ok;
 }
 
-constexpr int KVJ_WARPS = 8;
 constexpr int KVJ_UNROLL = 4;
+constexpr int kvj_threads(int warps) { return (warps < 8 ? 8 : warps) * 32; }
 
-// Joins the partial results of one (sequence, head, column): a warp takes every
-// KVJ_WARPS-th of them, KVJ_UNROLL in flight, a lane DH / 32 dimensions. It is
+// Joins the partial results of the columns of all (sequence, head)s: WARPS warps
+// a column (8 columns a block with one), each taking every WARPS-th of its
+// partial results, KVJ_UNROLL in flight, a lane DH / 32 dimensions. It is
 // launched while the attention still runs and waits for it here, so that its
-// start costs nothing. Bound by the latency of its reads: about 3.5 us, 10 us for
-// 512 partial results a column (with one warp of four reading one at a time 51).
-template <int DH>
-__global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_constant__ Kv4AttnArgs a) {
-  constexpr int E = DH / 32;
-  __shared__ float s_m[KVJ_WARPS], s_l[KVJ_WARPS], s_o[KVJ_WARPS][DH];
-  const int warp = warp_id(), lane = lane_id();
+// start costs nothing. Bound by the latency of its reads (kvj_warps).
+template <int DH, int WARPS>
+__global__ void __launch_bounds__(kvj_threads(WARPS)) kv4_join_kernel(const __grid_constant__ Kv4AttnArgs a) {
+  constexpr int E = DH / 32, COLS = kvj_threads(WARPS) / 32 / WARPS;
+  static_assert(WARPS == 1 || COLS == 1, "a block joins one column, or a warp does");
+  __shared__ float s_m[WARPS], s_l[WARPS], s_o[WARPS > 1 ? WARPS : 1][WARPS > 1 ? DH : 1];
+  const int warp = warp_id() % WARPS, lane = lane_id();
   const int rows = a.d.kv_heads * a.blocks_of_cols, group = a.heads / a.d.kv_heads;
-  const int kvh = blockIdx.x / a.cols, col = blockIdx.x - kvh * a.cols;
-  const int per = a.cols_block, cb = col / per, c = col - cb * per;
-  const int tok = col / group, head = kvh * group + col - tok * group;
+  const int all = a.d.kv_heads * a.cols, chunks = (all + COLS - 1) / COLS;
   grid_dependents_start();
   bool waited = false;
-  for (int beta = blockIdx.y; beta < a.d.b; beta += gridDim.y) {
-    uint32_t before;
-    const KvaSplit split = kva_split(a, beta, before);
-    const int nb = kva_blocks(a, beta), row = kvh * a.blocks_of_cols + cb;
+  int last = -1, nb = 0;
+  uint32_t before = 0;
+  KvaSplit split(0, 1);
+  auto column = [&](int beta, int x0) {
+    if (beta != last) {
+      split = kva_split(a, beta, before);
+      nb = kva_blocks(a, beta);
+      last = beta;
+    }
+    const bool real = x0 < all;
+    const int kvh = x0 / a.cols, col = x0 - kvh * a.cols;
+    const int per = a.cols_block, cb = col / per, c = col - cb * per;
+    const int tok = col / group, head = kvh * group + col - tok * group;
+    const int row = kvh * a.blocks_of_cols + cb;
     int w0 = 0, w1 = -1;
-    if (nb > 0) {
+    if (nb > 0 && real) {
       const uint32_t first = before + kva_first_block(row, nb);
       w0 = split.warp_of(first);
       w1 = split.warp_of(first + nb - 1);
@@ -748,12 +757,12 @@ __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_c
     }
     const long long at0 = ((long long)beta * rows + row) * a.cols_block + c;
     float m = -INFINITY, l = 0.f, o[E] = {};
-    for (int w = w0 + warp; w <= w1; w += KVJ_WARPS * KVJ_UNROLL) {
+    for (int w = w0 + warp; w <= w1; w += WARPS * KVJ_UNROLL) {
       float2 ml[KVJ_UNROLL];
       float x[KVJ_UNROLL][E];
 #pragma unroll
       for (int u = 0; u < KVJ_UNROLL; ++u) {
-        const int v = w + u * KVJ_WARPS;
+        const int v = w + u * WARPS;
         const long long at = at0 + (long long)v * a.cols_block;
         ml[u] = v <= w1 ? __ldcg(&a.part_ml[at]) : make_float2(-INFINITY, 0.f);
 #pragma unroll
@@ -775,30 +784,66 @@ __global__ void __launch_bounds__(KVJ_WARPS * 32) kv4_join_kernel(const __grid_c
         for (int e = 0; e < E; ++e) o[e] = fmaf(x[u][e], k, o[e]);
       }
     }
-    if (lane == 0) {
-      s_m[warp] = m;
-      s_l[warp] = l;
+    // a row that sees no token is zero
+    __nv_bfloat16* to = a.o + (((long long)beta * a.n + tok) * a.heads + head) * DH;
+    float* lse2 = a.lse2 == nullptr ? nullptr : a.lse2 + ((long long)beta * a.heads + head) * a.n + tok;
+    if constexpr (WARPS == 1) {
+      if (!real) return;
+#pragma unroll
+      for (int e = 0; e < E; ++e) to[e * 32 + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
+      if (lane == 0 && lse2 != nullptr) *lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+    } else {
+      if (lane == 0) {
+        s_m[warp] = m;
+        s_l[warp] = l;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
+      __syncthreads();
+      float top = s_m[0];
+#pragma unroll
+      for (int i = 1; i < WARPS; ++i) top = fmaxf(top, s_m[i]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) sum = fmaf(s_l[i], ex2_approx(s_m[i] - ref), sum);
+      const bool none = sum == 0.f;
+      if (threadIdx.x < DH) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) x = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - ref), x);
+        to[threadIdx.x] = __float2bfloat16_rn(none ? 0.f : x / sum);
+      }
+      if (threadIdx.x == 0 && lse2 != nullptr) *lse2 = none ? -INFINITY : ref + log2f(sum);
+      __syncthreads();
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
-    __syncthreads();
-    float top = s_m[0];
-#pragma unroll
-    for (int i = 1; i < KVJ_WARPS; ++i) top = fmaxf(top, s_m[i]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < KVJ_WARPS; ++i) sum = fmaf(s_l[i], ex2_approx(s_m[i] - ref), sum);
-    const bool none = sum == 0.f;  // a row that sees no token is zero
-    if (threadIdx.x < DH) {
-      float x = 0.f;
-#pragma unroll
-      for (int i = 0; i < KVJ_WARPS; ++i) x = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - ref), x);
-      a.o[(((long long)beta * a.n + tok) * a.heads + head) * DH + threadIdx.x] = __float2bfloat16_rn(none ? 0.f : x / sum);
+  };
+  if constexpr (WARPS == 1) {
+    // a run of columns a block, 8 at a time: they mostly share a sequence. (Their number is below 2^31: b n heads is.)
+    const unsigned items = (unsigned)a.d.b * (unsigned)chunks, each = items / gridDim.x, rest = items - each * gridDim.x;
+    const unsigned from = each * blockIdx.x + min(blockIdx.x, rest), until = from + each + (blockIdx.x < rest ? 1u : 0u);
+    for (unsigned item = from; item < until; ++item) {
+      const unsigned beta = item / (unsigned)chunks;
+      column((int)beta, (int)(item - beta * (unsigned)chunks) * COLS + warp_id());
     }
-    if (threadIdx.x == 0 && a.lse2 != nullptr) a.lse2[((long long)beta * a.heads + head) * a.n + tok] = none ? -INFINITY : ref + log2f(sum);
-    __syncthreads();
+  } else {
+    for (int beta = blockIdx.y; beta < a.d.b; beta += gridDim.y) column(beta, blockIdx.x);
   }
+}
+
+// Warps a column: one where blocks of 8 (4 of them fit an SM) would take a second
+// round, 32 where few columns have many partial results each. Device time of one
+// call, with 1, 8 and 32: 27520 columns 63, 174, 761 us; 1024 39.1, 44.6, 68; 768
+// 27.4, 28.1, 48; 512 37.3, 36.3, 51; 128 of 55 partial results 74, 65, 67; 64 of
+// 111 67, 47, 46; 32 of 222 64, 34, 30; 32 of 592 109, 31, 17.
+inline int kvj_warps(long long columns, long long segments, int max_warps) {
+  if (columns > KVA_MAX_SMS * 4) return 1;
+  return columns <= KVA_MAX_SMS * 2 && max_warps / segments > 64 ? 32 : 8;
+}
+
+inline KvaKernel kvj_kernel(int dh, int warps) {
+  if (dh == 128) return warps == 1 ? kv4_join_kernel<128, 1> : warps == 8 ? kv4_join_kernel<128, 8> : kv4_join_kernel<128, 32>;
+  return warps == 1 ? kv4_join_kernel<64, 1> : warps == 8 ? kv4_join_kernel<64, 8> : kv4_join_kernel<64, 32>;
 }
 
 struct Kv4WeightsArgs {
@@ -811,16 +856,16 @@ struct Kv4WeightsArgs {
 };
 
 // weights[u] += sum over the queries that share u's head of 2^(score - lse2):
-// KVW_VECTORS times 4 cached tokens a thread. Bound by the latency of its reads
-// (the scores come from L2 where they fit): what does not wait for the kernels
-// ahead is read before they end, the scores of two queries at a time after. 64
-// rows of about 27000 tokens, 4 queries each: 10 us, 16 with one vector a thread
-// and every read after the wait.
+// V times 4 cached tokens a thread. Bound by the latency of its reads (the scores
+// come from L2 where they fit): what does not wait for the kernels ahead is read
+// before they end, the scores of Q queries at a time after. 64 rows of about 27000
+// tokens, 4 queries each: 10 us with V = Q = 2, 16 with one vector a thread and
+// every read after the wait.
 constexpr int KVW_THREADS = 128;
-constexpr int KVW_VECTORS = 2;
 
-__global__ void __launch_bounds__(KVW_THREADS, 8) kv4_weights_kernel(const __grid_constant__ Kv4WeightsArgs a) {
-  constexpr int V = KVW_VECTORS, STEP = KVW_THREADS * 4;
+template <int V, int Q>
+__global__ void __launch_bounds__(KVW_THREADS, Q > 2 ? 4 : 8) kv4_weights_kernel(const __grid_constant__ Kv4WeightsArgs a) {
+  constexpr int STEP = KVW_THREADS * 4;
   const int group = a.heads / a.d.kv_heads, cols = group * a.n;
   const int key = blockIdx.x * STEP * V + threadIdx.x * 4;
   const int rows = a.d.b * a.d.kv_heads;
@@ -839,12 +884,12 @@ __global__ void __launch_bounds__(KVW_THREADS, 8) kv4_weights_kernel(const __gri
     const float* lse2 = a.lse2 + ((long long)beta * a.heads + kvh * group) * a.n;
     float sum[V][4] = {};
     int t = 0, h = 0;  // token and head of the next query
-    for (int c = 0; c < cols; c += 2) {
-      float4 x[2][V];
-      float l[2];
-      int seen[2];
+    for (int c = 0; c < cols; c += Q) {
+      float4 x[Q][V];
+      float l[Q];
+      int seen[Q];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < Q; ++k) {
         seen[k] = 0;
         if (c + k < cols) {
           seen[k] = kv4_seen(len, a.n, t, a.causal);
@@ -859,7 +904,7 @@ __global__ void __launch_bounds__(KVW_THREADS, 8) kv4_weights_kernel(const __gri
         }
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < Q; ++k)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const int at = key + v * STEP;
@@ -878,6 +923,14 @@ __global__ void __launch_bounds__(KVW_THREADS, 8) kv4_weights_kernel(const __gri
                                                           at + 3 < len ? old[v].w + sum[v][3] : old[v].w);
     }
   }
+}
+
+// Whether the blocks of <2, 2> are too few to hide the latency of a read, and the
+// queries many: <1, 8> then. Device time of the kernel with <2, 2> and <1, 8>: 18
+// blocks, 88 queries 24.1 and 9.8 us; 256 blocks, 8 queries 3.8 and 2.5; 864 blocks,
+// 22 queries 10.7 and 13.0; 472 blocks, 4 queries 4.4 and 5.6.
+inline bool kvw_few(long long rows, int capacity, int cols) {
+  return cols >= 8 && rows * ((capacity + KVW_THREADS * 8 - 1) / (KVW_THREADS * 8)) <= KVA_MAX_SMS * 4;
 }
 
 }  // namespace bpt

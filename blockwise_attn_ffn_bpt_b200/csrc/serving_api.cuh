@@ -420,15 +420,19 @@ int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void*
   }
   if (!L.direct) {
     LaunchScope ls("kv4_join", st);
-    const dim3 grid((unsigned)(kv_heads * L.cols), grid_y(b));
-    BPT_TRY(launch_kernel(dh == 128 ? kv4_join_kernel<128> : kv4_join_kernel<64>, a, grid, KVJ_WARPS * 32, 0, st));
+    const long long columns = (long long)b * kv_heads * L.cols;
+    const int warps = kvj_warps(columns, L.segments, L.max_warps), threads = kvj_threads(warps);
+    const long long runs = std::min<long long>((long long)b * ((kv_heads * L.cols + 7) / 8), KVA_MAX_SMS * 8);
+    const dim3 grid = warps == 1 ? dim3((unsigned)runs) : dim3((unsigned)(kv_heads * L.cols), grid_y(b));
+    BPT_TRY(launch_kernel(kvj_kernel(dh, warps), a, grid, threads, 0, st));
   }
   if (weights) {
     LaunchScope ls("kv4_weights", st);
     const Kv4WeightsArgs w{a.scores, a.lse2, weights, a.d, lens, n, heads, a.causal};
-    const int per = KVW_THREADS * 4 * KVW_VECTORS;
+    const bool few = kvw_few((long long)b * kv_heads, capacity, L.cols);
+    const int per = KVW_THREADS * 4 * (few ? 1 : 2);
     const dim3 grid((unsigned)((capacity + per - 1) / per), grid_y((long long)b * kv_heads));
-    BPT_TRY(launch_kernel(kv4_weights_kernel, w, grid, KVW_THREADS, 0, st));
+    BPT_TRY(launch_kernel(few ? kv4_weights_kernel<1, 8> : kv4_weights_kernel<2, 2>, w, grid, KVW_THREADS, 0, st));
   }
   return BPT_OK;
 }

@@ -233,6 +233,18 @@ def test_attention_over_long_caches(dh, heads, kv, n, lens, capacity):
                                                                  device="cuda"), rtol=1e-4)
 
 
+@pytest.mark.parametrize("dh,heads,kv,n", [(64, 9, 3, 25), (128, 80, 16, 8), (64, 96, 96, 1), (128, 20, 20, 3)])
+def test_attention_of_many_queries_over_short_contexts(dh, heads, kv, n):
+    # more results than the device has blocks: a warp joins a column, several a block, the last ones of a sequence not a
+    # whole block's; some columns' heads have no token
+    lens = [93, 1, 0, 64, 65, 300, 7, 128, 0, 33, 90, 2, 5]
+    cache, held = filled(len(lens), kv, dh, lens, 320, seed=81)
+    q = bf16((len(lens), n, heads * dh), 82)
+    w = torch.rand((len(lens), kv, 320), generator=torch.Generator().manual_seed(1)).cuda()
+    check_attention(q, cache, held, lens, heads)
+    check_attention(q, cache, held, lens, heads, weights=w)
+
+
 def test_attention_with_large_and_equal_scores():
     # scores of about a thousand, whose exponentials overflow without the maximum, and equal ones: o is V's mean
     for dh in (64, 128):
