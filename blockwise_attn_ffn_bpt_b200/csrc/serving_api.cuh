@@ -247,12 +247,13 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
   a.rot = rot;
   a.units = (heads + kv_heads) * (dh / (2 * w));
   while ((1 << a.head_shift) < dh / (2 * w)) ++a.head_shift;
-  // tokens of a block: up to what its table of angles holds, as long as that
-  // leaves a few rounds of blocks for every SM; a token of very many heads is
-  // shared by several blocks
+  // tokens of a block: up to what its table of angles holds, as many as give every
+  // thread a unit, and more as long as that leaves a few rounds of blocks for every
+  // SM (5490 tokens of 4 heads of 64 in fp32, 32 units each, took 13.4 us with a
+  // token a block, 5.8 with 8); a token of very many heads is shared by several blocks
   a.chunk = std::min(a.units, ROT_CHUNK);
   const long long blocks = (long long)KVA_MAX_SMS * ROT_BLOCKS * ROT_ROUNDS;
-  a.tile = (int)std::max<long long>(1, std::min<long long>(ROT_TABLE / (rot / 2), a.tokens / blocks));
+  a.tile = (int)std::max<long long>(1, std::min<long long>(ROT_TABLE / (rot / 2), std::max<long long>(ROT_THREADS / a.units, a.tokens / blocks)));
   a.positions = positions;
   a.pos64 = position_bytes == 8;
   a.pos_stride = position_stride;
