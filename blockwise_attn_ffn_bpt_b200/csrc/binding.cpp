@@ -96,6 +96,8 @@ struct Cache {
     const at::Tensor& t = *data;
     if (!t.is_cuda() || t.scalar_type() != at::kByte || t.dim() != 4 || !t.is_contiguous())
       refuse(PyExc_ValueError, name, " must be a contiguous uint8 CUDA tensor of 4 dimensions");
+    if ((dh != 64 && dh != 128) || t.size(3) != 72 * dh)
+      refuse(PyExc_ValueError, name, "'s blocks are ", t.size(3), " bytes, which is not 72 dh for dh = ", dh);
     b = count_of(t.size(0), "b");
     kv_heads = count_of(t.size(1), "kv_heads");
     capacity = count_of(t.size(2) * 64, "capacity");

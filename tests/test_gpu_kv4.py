@@ -486,6 +486,22 @@ def test_captured_behind_copies_fills_and_other_streams():
     assert bpt.stream_status() == 0
 
 
+def test_a_cache_that_is_not_what_it_says_is_refused():
+    cache, other = bpt.kv4_cache(1, 2, 64, 64), bpt.kv4_cache(1, 2, 64, 128)
+    k, n = bf16((1, 1, 2 * 64), 0), ints(0)
+    wide = bf16((1, 1, 2 * 128), 0)
+    cache.dh = 128
+    for call in (lambda: bpt.kv4_store(cache, wide, wide, n), lambda: bpt.kv4_load(cache, n, 1),
+                 lambda: bpt.kv4_attention(wide, cache, n, 2),
+                 lambda: bpt.kv4_evict(other, torch.zeros((1, 2, 64), device="cuda"), n, 8, 1, cache)):
+        with pytest.raises(ValueError, match="blocks are 4608 bytes"):
+            call()
+    cache.dh, cache.data = 64, cache.data[..., :64]
+    with pytest.raises(ValueError, match="contiguous uint8"):
+        bpt.kv4_store(cache, k, k, n)
+    assert bpt.stream_status() == 0
+
+
 def test_two_streams_at_once():
     lens = [1000, 400]
     cache, _ = filled(2, 4, 64, lens, 1024, seed=17)
