@@ -18,11 +18,12 @@
 namespace bpt {
 
 constexpr int EVICT_THREADS = 1024;
+constexpr int EVICT_SHORT = 256;  // threads for many short rows (evict_threads)
 constexpr int EVICT_BINS = 2048;
 // Copies of the histogram, one to every second or fourth lane: weights of a few
 // octaves share few bins of the first digit, and lanes that add to one bin take
 // turns. (48 KB of it and of the cluster's totals are there without asking.)
-constexpr int evict_copies(int cl) { return cl > 1 ? 2 : 4; }
+constexpr int evict_copies(int cl, int threads) { return cl > 1 || threads == EVICT_SHORT ? 2 : 4; }
 constexpr int EVICT_CACHED = 40960;  // tokens of a block whose keys stay in shared memory (160 KB)
 
 struct Kv4SelectArgs {
@@ -64,10 +65,11 @@ __device__ __forceinline__ uint4 weight_keys(const float4& w, int i, int old) {
 // A cluster of CL blocks a (sequence, head), each with an equal part of its
 // tokens. The keys of up to EVICT_CACHED tokens a block stay in shared memory
 // after the first pass; longer rows are read again, from L2.
-template <int CL, bool CACHED>
-__global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_constant__ Kv4SelectArgs a) {
+template <int CL, bool CACHED, int THREADS>
+__global__ void __launch_bounds__(THREADS) kv4_select_kernel(const __grid_constant__ Kv4SelectArgs a) {
   extern __shared__ uint4 cached[];
-  constexpr int COPIES = evict_copies(CL);
+  constexpr int COPIES = evict_copies(CL, THREADS), PER = EVICT_BINS / THREADS;  // bins of a thread
+  static_assert(CL == 1 || PER == 2, "clusters read two bins a thread");
   __shared__ int hist[COPIES][EVICT_BINS];
   __shared__ int warp_sum[32], warp_tie[32];
   __shared__ int s_bin, s_need, s_count;
@@ -88,10 +90,10 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
     const float* w = a.weights + (long long)row * a.d.capacity;
     int* kept = a.kept + (long long)row * a.keep;
     if (rank == 0 && tid == 0 && row == beta * a.d.kv_heads) a.lens_out[beta] = left;
-    const int first = rank * EVICT_THREADS + tid;
-    for (int i = need + first; i < a.keep; i += CL * EVICT_THREADS) kept[i] = i < left ? old + i - need : -1;
+    const int first = rank * THREADS + tid;
+    for (int i = need + first; i < a.keep; i += CL * THREADS) kept[i] = i < left ? old + i - need : -1;
     if (need == old) {
-      for (int i = first; i < need; i += CL * EVICT_THREADS) kept[i] = i;
+      for (int i = first; i < need; i += CL * THREADS) kept[i] = i;
       continue;
     }
     if (need == 0) continue;
@@ -111,13 +113,13 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       const uint32_t digit = (1u << bits) - 1;
       __syncthreads();
-      for (int i = tid; i < COPIES * EVICT_BINS; i += EVICT_THREADS) (&hist[0][0])[i] = 0;
+      for (int i = tid; i < COPIES * EVICT_BINS; i += THREADS) (&hist[0][0])[i] = 0;
       __syncthreads();
       auto count = [&](uint32_t key) {
         if ((key & mask) == prefix) atomicAdd(&hist[lane % COPIES][(key >> shift) & digit], 1);
       };
 #pragma unroll 4
-      for (int i = tid; i < quads; i += EVICT_THREADS) {
+      for (int i = tid; i < quads; i += THREADS) {
         const uint4 k = keys_of(i, pass == 0);
         count(k.x);
         count(k.y);
@@ -125,28 +127,30 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
         count(k.w);
       }
       __syncthreads();
-      // from the top: thread i holds bins BINS - 1 - 2i and BINS - 2 - 2i
-      const int top = EVICT_BINS - 1 - 2 * tid;
-      int hi = 0, lo = 0;
+      // from the top: thread i holds the PER bins from BINS - 1 - PER i down
+      const int top = EVICT_BINS - 1 - PER * tid;
+      int bin[PER] = {};
 #pragma unroll
-      for (int x = 0; x < COPIES; ++x) {
-        hi += hist[x][top];
-        lo += hist[x][top - 1];
-      }
+      for (int p = 0; p < PER; ++p)
+#pragma unroll
+        for (int x = 0; x < COPIES; ++x) bin[p] += hist[x][top - p];
       if constexpr (CL > 1) {
         int* mine = s_total[pass & 1];
-        mine[top] = hi;
-        mine[top - 1] = lo;
+        mine[top] = bin[0];
+        mine[top - 1] = bin[1];
         cluster_sync_all();
-        hi = lo = 0;
+        bin[0] = bin[1] = 0;
 #pragma unroll
         for (int r = 0; r < CL; ++r) {
           const int2 x = cluster_load2(smem_addr(mine + top - 1), r);
-          lo += x.x;
-          hi += x.y;
+          bin[1] += x.x;
+          bin[0] += x.y;
         }
       }
-      int sum = hi + lo;
+      int all = 0;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) all += bin[p];
+      int sum = all;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, sum, o);
@@ -154,12 +158,17 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
       }
       if (lane == 31) warp_sum[warp] = sum;
       __syncthreads();
-      const int before = sum - hi - lo + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
-      if (before < want && want <= before + hi + lo) {  // exactly one thread
-        const bool in_hi = want <= before + hi;
-        s_bin = EVICT_BINS - (in_hi ? 1 : 2) - 2 * tid;
-        s_need = want - before - (in_hi ? 0 : hi);
-        s_count = in_hi ? hi : lo;
+      int before = sum - all + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
+      if (before < want && want <= before + all) {  // exactly one thread
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+          if (before < want && want <= before + bin[p]) {
+            s_bin = top - p;
+            s_need = want - before;
+            s_count = bin[p];
+          }
+          before += bin[p];
+        }
       }
       __syncthreads();
       prefix |= (uint32_t)s_bin << shift;
@@ -173,7 +182,7 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
     }
     // keys above `prefix` stay, and the first `want` of those equal to it;
     // each warp takes a run of whole 128s and first counts what stays before it
-    const int run = (quads + 1023) / 1024 * 32;
+    const int run = (quads + THREADS - 1) / THREADS * 32;
     const int lo = min(warp * run, quads), hi = min(lo + run, quads);
     int more = 0, tie = 0;
 #pragma unroll 4
@@ -192,7 +201,7 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_select_kernel(const __grid_
     int above = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
     int ties = __reduce_add_sync(0xffffffffu, lane < warp ? warp_tie[lane] : 0);
     if constexpr (CL > 1) {
-      if (tid == EVICT_THREADS - 1) {
+      if (tid == THREADS - 1) {
         s_above = above + more;
         s_ties = ties + tie;
       }
@@ -258,17 +267,26 @@ inline int evict_cluster(long long rows, int capacity) {
   return rows * 4 <= KVA_MAX_SMS ? 4 : rows * 2 <= KVA_MAX_SMS ? 2 : 1;
 }
 
+// Threads of a block: few where the rows, two blocks of 1024 an SM, would take a
+// second round, and are short. Device time of the selection, 1024 against 256: 1440
+// rows of 512 tokens 42.6, 20.4 us; 1024 of 2048 34.4, 22.2, of 4096 38.6, 28.8; 296
+// of 4096 12.3, 13.2; 64 of 2048 5.3, 6.7.
+inline int evict_threads(int cl, long long rows, int capacity) {
+  return cl == 1 && rows > KVA_MAX_SMS * 2 && capacity <= 4096 ? EVICT_SHORT : EVICT_THREADS;
+}
+
 typedef void (*EvictKernel)(const Kv4SelectArgs);
-inline EvictKernel evict_kernel(int cl, bool cached) {
-  if (cl == 4) return cached ? kv4_select_kernel<4, true> : kv4_select_kernel<4, false>;
-  if (cl == 2) return cached ? kv4_select_kernel<2, true> : kv4_select_kernel<2, false>;
-  return cached ? kv4_select_kernel<1, true> : kv4_select_kernel<1, false>;
+inline EvictKernel evict_kernel(int cl, bool cached, int threads) {
+  if (threads == EVICT_SHORT) return kv4_select_kernel<1, true, EVICT_SHORT>;  // such rows are always cached
+  if (cl == 4) return cached ? kv4_select_kernel<4, true, EVICT_THREADS> : kv4_select_kernel<4, false, EVICT_THREADS>;
+  if (cl == 2) return cached ? kv4_select_kernel<2, true, EVICT_THREADS> : kv4_select_kernel<2, false, EVICT_THREADS>;
+  return cached ? kv4_select_kernel<1, true, EVICT_THREADS> : kv4_select_kernel<1, false, EVICT_THREADS>;
 }
 
 inline bool evict_set_attributes() {
   bool ok = true;
   for (int cl : {1, 2, 4})
-    ok = ok && cudaFuncSetAttribute(evict_kernel(cl, true), cudaFuncAttributeMaxDynamicSharedMemorySize,
+    ok = ok && cudaFuncSetAttribute(evict_kernel(cl, true, EVICT_THREADS), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     EVICT_CACHED * 4) == cudaSuccess;
   return ok;
 }

@@ -476,8 +476,9 @@ int bpt_kv4_evict(const void* cache, const float* weights, const int* lens, int 
     const int cl = evict_cluster((long long)rows, capacity);
     const size_t share = (size_t)(capacity / 4 + cl - 1) / cl * 4;  // tokens of a block
     const bool cached = share <= EVICT_CACHED;
-    BPT_TRY(launch_kernel(evict_kernel(cl, cached), a, dim3((unsigned)rows * cl), EVICT_THREADS, cached ? share * 4 : 0, st,
-                          cl));
+    const int threads = evict_threads(cl, (long long)rows, capacity);
+    BPT_TRY(launch_kernel(evict_kernel(cl, cached, threads), a, dim3((unsigned)rows * cl), threads, cached ? share * 4 : 0,
+                          st, cl));
   }
   {
     LaunchScope ls("kv4_move", st);

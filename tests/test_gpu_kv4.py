@@ -571,6 +571,19 @@ def test_evict_ties_signs_infinities_and_nan():
         check_evict(64, 1, [320, 300, 317], 320, keep, 2, 320, w.cuda())
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal", "odd values"])
+@pytest.mark.parametrize("capacity,keep", [(64, 1), (512, 200), (4096, 1500)])
+def test_evict_from_many_short_rows(capacity, keep, kind):
+    # more rows than two blocks an SM
+    lens = [capacity - 7 * i for i in range(8)] + [0, 1]
+    g = torch.Generator().manual_seed(capacity)
+    w = torch.randn((len(lens), 31, capacity), generator=g)
+    w = {"spread": w.mul(3).exp(), "ties": w.mul(2).round(), "equal": torch.zeros_like(w), "odd values": w}[kind]
+    if kind == "odd values":
+        w[:, :, ::5], w[:, 3, 1::5], w[:, 4, 2::7] = -0.0, float("nan"), -float("inf")
+    check_evict(64, 31, lens, capacity, keep, keep // 9, capacity, w.cuda(), rows=False)
+
+
 @pytest.mark.parametrize("length,heads", [(1023, 2), (1025, 2), (5000, 2), (33333, 2), (16390, 40), (16390, 80),
                                           (200001, 1)])
 @pytest.mark.parametrize("ties", [False, True])
