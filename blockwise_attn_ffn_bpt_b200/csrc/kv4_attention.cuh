@@ -33,7 +33,10 @@
 // is taken off it, and the second sum is of p mid, mid = min + 7.5 scale. (At
 // 32768 tokens of equal weight o was 1.6e-2 off in the norm with an offset of
 // 135 P' a token in that sum until its end; the rounding of o to bf16 alone is
-// 1.7e-3.)
+// 1.7e-3.) The sum taken off is that of the fp16 numbers that met the codes, so
+// that a rounding error meets code - 7.5, which is of either sign: P' of nearly
+// equal weights all round the same way. (With scores within 1e-4 at 20000 tokens
+// o was 5.5e-2 off in the norm with the sum of the P' before their rounding.)
 //
 // The cached blocks of all sequences and heads, one after the other, are split
 // evenly over the warps of the device, whatever the lengths. A warp works on
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
     // sums of a lane are of its own tokens until the end of the run
     float o[NT][G][4][4] = {};
     float m[NT][2], ref[NT][2] = {}, l[NT][2] = {}, off[NT][G][2] = {};  // ref: m score_scale, or 0 for none
-    float part[NT][G][2] = {};  // sums of P' not yet taken off o
+    float part[NT][G][2] = {};  // sums of w P', as rounded, not yet taken off o
     float wide[NT][G][2];  // w of the comment above
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -454,11 +457,11 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 #pragma unroll
             for (int gi = 0; gi < G; ++gi) {
               off[nt][gi][e] *= f;
-              part[nt][gi][e] *= f;
               // the P' so far fall by f: w rises by as much and their sum stays, as long as w can
               float& w = wide[nt][gi][e];
               const float more = w * back, now_o = more <= KVA_WIDEST ? 1.0f : __fdividef(KVA_WIDEST * f, w);
               w = fminf(more, KVA_WIDEST);
+              part[nt][gi][e] *= now_o;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 o[nt][gi][i][e] *= now_o;
@@ -492,7 +495,6 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
               // a token that is not seen may have any parameters, NaN among them
               const bool live = WHOLE || key0 + ra + (e >> 1) * 8 < lim[nt][e & 1];
               if (!live) y[gi][e] = 0.f;
-              part[nt][gi][e & 1] += y[gi][e];
               if (live) off[nt][gi][e & 1] = fmaf(p[e], fmaf(7.5f, scale_of(pr), min_of(pr)), off[nt][gi][e & 1]);
             }
             high = max3f(high, y[gi][0] * wide[nt][gi][0], y[gi][1] * wide[nt][gi][1]);
@@ -510,6 +512,7 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
                 if (top * w > KVA_HIGH) {  // the power of two that takes it to 2^7
                   const float less = __int_as_float((261 - (__float_as_int(top) >> 23)) << 23), now_o = __fdividef(less, w);
                   w = less;
+                  part[nt][gi][e] *= now_o;
 #pragma unroll
                   for (int i = 0; i < 4; ++i) {
                     o[nt][gi][i][e] *= now_o;
@@ -521,8 +524,13 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
 #pragma unroll
           for (int gi = 0; gi < G; ++gi)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-              bf[nt][gi][x] = transpose8(pack_half2(y[gi][2 * x] * wide[nt][gi][0], y[gi][2 * x + 1] * wide[nt][gi][1]));
+            for (int x = 0; x < 2; ++x) {
+              const __half2 two = __floats2half2_rn(y[gi][2 * x] * wide[nt][gi][0], y[gi][2 * x + 1] * wide[nt][gi][1]);
+              const float2 rounded = __half22float2(two);
+              part[nt][gi][0] += rounded.x;
+              part[nt][gi][1] += rounded.y;
+              bf[nt][gi][x] = transpose8(*reinterpret_cast<const uint32_t*>(&two));
+            }
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) {
@@ -563,14 +571,14 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       for (int y = CW / 2; y < 4; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
       return x;
     };
-    auto centre = [&]() {  // takes 7.5 sum P' off o (off its first copy)
+    auto centre = [&]() {  // takes 7.5 times the sum of the rounded P' off o (off its first copy)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int gi = 0; gi < G; ++gi)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float all = over_lanes(part[nt][gi][e]) * wide[nt][gi][e];
+            const float all = over_lanes(part[nt][gi][e]);
             part[nt][gi][e] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -620,11 +628,11 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
         if (real && g == 0) (DIRECT ? own_ml + c : a.part_ml + to)[0] = make_float2(m[nt][e] * a.score_scale, sum);
 #pragma unroll
         for (int gi = 0; gi < G; ++gi) {
-          const float add = over_lanes(fmaf(-7.5f, part[nt][gi][e], off[nt][gi][e]));
+          const float per = 1.0f / wide[nt][gi][e], add = over_lanes(fmaf(-7.5f * per, part[nt][gi][e], off[nt][gi][e]));
           float x[8];  // dimensions 8u .. 8u + 7 of word u = 8 gi + g
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float unit = i % 2 ? 0x1p20f : 0x1p24f, per = 1.0f / wide[nt][gi][e];
+            const float unit = i % 2 ? 0x1p20f : 0x1p24f;
             x[i] = fmaf(over_copies(o[nt][gi][i][e]) * unit, per, add);
             x[i + 4] = fmaf(over_copies(o[nt][gi][i][e + 2]) * unit, per, add);
           }

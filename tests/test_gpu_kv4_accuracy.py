@@ -1,0 +1,55 @@
+"""How exact the 4-bit attention's output is where errors of its weights could add up over a long cache.
+
+Per head, in the 2-norm over its dimensions, relative to o:
+* o's rounding to bf16: at most 2^-8;
+* the weights' products with V's scale enter as fp16, off by at most 2^-11 of themselves. An error e of a product meets
+  the token's code less 7.5 (the kernel takes off 7.5 of the same rounded product), which is of either sign; with values
+  that are independent of the weights the sum of the e (code - 7.5) is to the sum of the products times (code - 7.5) at
+  most as their sizes, 2^-11, and that sum is to o about as one to one: within 2^-10.
+Both fall with o as the cache grows. A sum of errors of one sign does not: 2^-11 of 7.5 scale is far above o then.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import blockwise_attn_ffn_bpt_b200 as bpt
+from oracle import serving_oracle as so
+
+pytestmark = pytest.mark.gpu
+
+NORM = 2.0 ** -8 + 2.0 ** -10
+
+
+def heads_of(x, heads):
+    return x.double().cpu().numpy().reshape(x.shape[0], x.shape[1], heads, x.shape[2] // heads)
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("b,kv,group,length", [(1, 2, 1, 20000), (1, 2, 4, 20000), (1, 1, 16, 20000), (3, 32, 1, 3000)])
+@pytest.mark.parametrize("kind", ["scores within 1e-4", "every 64th token above equal ones"])
+def test_nearly_equal_weights_over_a_long_cache(kind, b, kv, group, length, dh):
+    # the split over the device with 1, 4 and 16 queries a head, and a thread block a head
+    g = torch.Generator().manual_seed(length + dh)
+    heads, c = kv * group, np.log2(np.e) / np.sqrt(dh)
+    v = torch.randn((b, length, kv * dh), generator=g).bfloat16()
+    if kind == "scores within 1e-4":
+        k = torch.randn((b, length, kv * dh), generator=g).bfloat16()
+        q = (torch.randn((b, 1, heads * dh), generator=g) * (1e-4 / (c * dh ** 0.5))).bfloat16()
+    else:
+        k = torch.zeros((b, length, kv * dh), dtype=torch.bfloat16)
+        k[:, ::64] = 3.3 / (c * dh)
+        q = torch.ones((b, 1, heads * dh), dtype=torch.bfloat16)
+    cache = bpt.kv4_cache(b, kv, length, dh)
+    zero = torch.zeros(b, dtype=torch.int32, device="cuda")
+    bpt.kv4_store(cache, k.cuda(), v.cuda(), zero)
+    o = heads_of(bpt.kv4_attention(q.cuda(), cache, zero + length, heads), heads)
+    assert bpt.stream_status() == 0
+    qn = heads_of(q, heads)
+    for i in range(b):
+        for h in sorted({0, kv - 1}):
+            kn, vn = (so.values(*so.quantise(heads_of(x[i:i + 1], kv)[0, :, h])) for x in (k, v))
+            for x in range(h * group, (h + 1) * group):
+                ref, _, _ = so.attention(qn[i, :, x:x + 1], kn[None], vn[None], True)
+                err = np.linalg.norm(o[i, 0, x] - ref[0, 0]) / np.linalg.norm(ref)
+                assert err <= NORM, f"sequence {i}, head {x}: o is {err:.2e} off"
