@@ -571,18 +571,20 @@ __global__ void __launch_bounds__(KvaCfg<DH, NT>::WARPS * 32, 1) kv4_attention_k
       for (int y = CW / 2; y < 4; y <<= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
       return x;
     };
-    auto centre = [&]() {  // takes 7.5 times the sum of the rounded P' off o (off its first copy)
+    auto centre = [&]() {  // takes 7.5 times the sum of the rounded P' off o, off each copy its own
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int gi = 0; gi < G; ++gi)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float all = over_lanes(part[nt][gi][e]);
+            float all = part[nt][gi][e];
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) all += __shfl_xor_sync(0xffffffffu, all, y);
             part[nt][gi][e] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float x = fold == 0 ? all * (i % 2 ? -7.5f * 0x1p-20f : -7.5f * 0x1p-24f) : 0.f;
+              const float x = all * (i % 2 ? -7.5f * 0x1p-20f : -7.5f * 0x1p-24f);
               o[nt][gi][i][e] += x;
               o[nt][gi][i][e + 2] += x;
             }

@@ -53,3 +53,32 @@ def test_nearly_equal_weights_over_a_long_cache(kind, b, kv, group, length, dh):
                 ref, _, _ = so.attention(qn[i, :, x:x + 1], kn[None], vn[None], True)
                 err = np.linalg.norm(o[i, 0, x] - ref[0, 0]) / np.linalg.norm(ref)
                 assert err <= NORM, f"sequence {i}, head {x}: o is {err:.2e} off"
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("group", [1, 4, 8, 12])
+def test_values_that_cancel_over_a_very_long_cache(group, dh):
+    # Tokens in pairs of the same key and opposite values, both exact in the cache: o is 0, a pair's weights are rounded
+    # alike, and what is left is what the sums of weight times code lose. These grow for 16 blocks at most until their
+    # mean is taken off: to 15 times the products of 1024 tokens, or of the half or quarter of them that each of 2 or 4
+    # copies of the queries meets (up to 4 and 2 queries a head). Each product of 16 tokens loses at most a last place of
+    # the sum, 2^-23 of it. Relative to the sum of the weights, with scales below 2, that is 2^-23 15 (1024 / copies) / 16 2.
+    # 256 heads of 131072 tokens, the same 64 over and over, are 200 blocks and more for every warp.
+    b, kv, blocks = 8, 32, 2048
+    g = torch.Generator().manual_seed(dh)
+    x = torch.randint(0, 16, (b, 32, kv, dh // 64, 64), generator=g) - 7.5
+    x[..., 0], x[..., 1] = -7.5, 7.5
+    x = (x * (1 + torch.randint(0, 8, (b, 32, kv, dh // 64, 1), generator=g) / 8)).reshape(b, 32, 1, kv * dh)
+    v = torch.cat((x, -x), 2).view(b, 64, kv * dh)
+    assert torch.equal(v, v.bfloat16().float())
+    k = torch.randn((b, 32, kv * dh), generator=g).bfloat16().repeat_interleave(2, 1)
+    small = bpt.kv4_cache(b, kv, 64, dh)
+    zero = torch.zeros(b, dtype=torch.int32, device="cuda")
+    bpt.kv4_store(small, k.cuda(), v.bfloat16().cuda(), zero)
+    cache = bpt.KV4Cache(small.data.repeat(1, 1, blocks, 1), dh)
+    q = torch.randn((b, 1, kv * group * dh), generator=g).bfloat16().cuda()
+    o = bpt.kv4_attention(q, cache, zero + 64 * blocks, kv * group)
+    assert bpt.stream_status() == 0
+    copies = 4 if group <= 2 else 2 if group <= 4 else 1
+    most = o.float().abs().max().item()
+    assert most <= 2.0 ** -23 * 15 * (1024 / copies) / 16 * 2, f"{most:.2e}"
