@@ -26,7 +26,8 @@
 // of its column and group, w P' being at most 2^14 and 2^7 where w is set: what
 // lies 2^-31 below the largest P' so far is lost, everything above 2^-21 of it
 // keeps fp16's 11 bits. w falls when a P' would pass 2^14, and rises with the
-// softmax's maximum, which takes the P' of the tokens before with it.
+// softmax's maximum, which takes the P' of the tokens before with it; it is at
+// most 2^125, so that of the smallest scales 2^-150 is lost, as fp32 does itself.
 //
 // The sum of P' code, 7.5 times that of P' and more, would lose the values' small
 // mean over many tokens in its roundings. So every KVA_CENTRE blocks 7.5 sum P'
@@ -71,7 +72,7 @@ constexpr int KVA_MAX_SMS = 148;      // the split does not grow past it (worksp
 // 417.6 us, with 8 2.4e-4 and 418.2, with 4 2.2e-4 (2e-4 of it the weights' fp16)
 // and 419.7; with 512 heads 757, 759 and 764 us.
 constexpr int KVA_CENTRE = 8;
-constexpr float KVA_HIGH = 16384.0f, KVA_WIDEST = 0x1p100f;  // of w P' and of w
+constexpr float KVA_HIGH = 16384.0f, KVA_WIDEST = 0x1p125f;  // of w P' and of w (whose reciprocal is a normal number)
 constexpr float KVA_LAZY = 8.0f;      // the maximum is raised when a score passes it by this (log2)
 
 // Warps of an SM and stages of a warp: the rings take 216 KB in every case, and

@@ -543,7 +543,9 @@ int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, c
  * lens[beta] are left as they are). The scores and all sums are fp32. q (below
  * 2^120) enters its products as fp16, relative to its largest element; so does
  * each softmax weight times a token's scale of V, relative to the largest such
- * product of the column and its 64 dimensions, of which 2^-31 is lost.
+ * product of the column and its 64 dimensions, of which 2^-31, or 2^-150 where
+ * that is more, is lost. V is below 2^96: weights of up to 2^8 are summed over
+ * the tokens before the division.
  * workspace: bpt_kv4_attention_workspace_bytes of the same arguments, which may
  * be 0 (short caches without weights; workspace may then be NULL). */
 size_t bpt_kv4_attention_workspace_bytes(int b, int n, int heads, int kv_heads, int capacity, int dh,

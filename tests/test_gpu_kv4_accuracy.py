@@ -82,3 +82,36 @@ def test_values_that_cancel_over_a_very_long_cache(group, dh):
     copies = 4 if group <= 2 else 2 if group <= 4 else 1
     most = o.float().abs().max().item()
     assert most <= 2.0 ** -23 * 15 * (1024 / copies) / 16 * 2, f"{most:.2e}"
+
+
+@pytest.mark.parametrize("capacity", [512, 20032])
+@pytest.mark.parametrize("size", [-95, -108, -116, -121])
+@pytest.mark.parametrize("low", [-13, -20])
+def test_values_near_the_smallest_scale(size, low, capacity):
+    # one token of score 0 and no value, and many `low` (log2) below it, with V's scales down to the smallest that the
+    # cache keeps.
+    # Bounds: o's rounding, where it may be subnormal (half a step is 2^-134 then); the products' fp16 rounding, 2^-11 of
+    # 15 p scale; scores and exponentials 2^-18; and 2^-31 of the largest product, or 2^-150, lost of each token's.
+    n, dh = 400, 128
+    g = np.random.default_rng(-size)
+    v = torch.tensor(g.standard_normal((1, n, dh)) * 2.0 ** size).float().bfloat16()
+    v[:, 130] = 0
+    score = np.where(np.arange(n) == 130, 0.0, low) * np.log(2) / np.sqrt(dh)  # times a query of ones
+    k = torch.tensor(np.broadcast_to(score[:, None], (n, dh))[None].copy()).float().bfloat16()
+    cache = bpt.kv4_cache(1, 1, capacity, dh)
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bpt.kv4_store(cache, k.cuda(), v.cuda(), zero)
+    q = torch.ones((1, 1, dh), dtype=torch.bfloat16, device="cuda")
+    o = heads_of(bpt.kv4_attention(q, cache, zero + n, 1), 1)[0, 0, 0]
+    (kc, ks, km), (vc, vs, vm) = (so.quantise(heads_of(x, 1)[0, :, 0]) for x in (k, v))
+    assert (np.delete(vs, 130, 0) >= 2.0 ** -126).all()
+    s = so.values(kc, ks, km) @ np.ones(dh) / np.sqrt(dh)
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    step, mid = np.repeat(vs, 64, -1), np.repeat(np.abs(vm), 64, -1)
+    ref = p @ so.values(vc, vs, vm)
+    tol = (2.0 ** -8 * np.abs(ref) + 2.0 ** -134 + 2.0 ** -11 * (p @ (15 * step)) + 2.0 ** -18 * (p @ (mid + 15 * step))
+           + n * 15 * np.maximum(2.0 ** -31 * (p[:, None] * step).max(0), 2.0 ** -150))
+    err = np.abs(o - ref)
+    assert (err <= tol).all(), f"{(err / tol).max():.2f} times the bound"
+    assert bpt.stream_status() == 0
