@@ -81,6 +81,56 @@ struct Kv4StoreArgs {
   int* status;
 };
 
+// rint((x - lo) r) of the exact difference, where that has more bits than fp32.
+__device__ __forceinline__ uint32_t kv4_code_wide(float x, float lo, float r) {
+  // the difference as a sum of two (Knuth's two-sum), each times r exact in fp64
+  const float d = __fsub_rn(x, lo), b = __fsub_rn(d, x);
+  const float rest = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(lo, b));
+  const double p = (double)d * (double)r, more = (double)rest * (double)r;
+  double c = rint(p);
+  const double f = p - c;  // exact; within half of c, and `more` may lead out of that
+  const bool odd = (int)c & 1;
+  if (more > 0.5 - f || (odd && more == 0.5 - f && more != 0.0)) c += 1.0;
+  else if (more < -0.5 - f || (odd && more == -0.5 - f && more != 0.0)) c -= 1.0;
+  return (uint32_t)c;
+}
+
+// Whether a code of 16 values may depend on what their fp32 difference from lo
+// leaves out: that is not zero, and the product without it next to a tie. (Calls,
+// not inline: 16 values' codes in fp64 take the store from 40 registers to 69 and
+// the example below from 64 to 84 us, were they in its line.)
+__device__ __noinline__ bool kv4_near_tie(uint4 xs, uint4 ys, float lo, float r) {
+  const uint32_t raw[8] = {xs.x, xs.y, xs.z, xs.w, ys.x, ys.y, ys.z, ys.w};
+  const uint64_t minus = f2_pack(-lo, -lo), times = f2_pack(r, r), neg = f2_pack(-1.0f, -1.0f);
+  const uint64_t magic = f2_pack(12582912.0f, 12582912.0f);
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t x = f2_pack(__uint_as_float(raw[i] << 16), __uint_as_float(raw[i] & 0xffff0000u));
+    const uint64_t d = f2_add(x, minus), b = f2_fma(x, neg, d);
+    const uint64_t rest = f2_add(f2_fma(f2_fma(b, neg, d), neg, x), f2_fma(b, neg, minus));
+    const uint64_t away = f2_fma(d, times, f2_fma(f2_fma(d, times, magic), neg, magic));  // from the code
+    float r0, r1, a0, a1;
+    f2_unpack(rest, r0, r1);
+    f2_unpack(away, a0, a1);
+    // what is left out moves the product by 16 times 2^-24 at most
+    near |= (r0 != 0.f && fabsf(a0) > 0.49999f) || (r1 != 0.f && fabsf(a1) > 0.49999f);
+  }
+  return near;
+}
+
+// The codes of 16 values, as two words, where kv4_near_tie.
+__device__ __noinline__ uint2 kv4_words_wide(uint4 x, uint4 y, float lo, float r) {
+  uint32_t word[2] = {};
+  const uint32_t raw[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    word[i / 4] = word[i / 4] * 16u + kv4_code_wide(__uint_as_float(raw[i] & 0xffff0000u), lo, r);
+    word[i / 4] = word[i / 4] * 16u + kv4_code_wide(__uint_as_float(raw[i] << 16), lo, r);
+  }
+  return make_uint2(word[0], word[1]);
+}
+
 // 16 values of x (bf16, packed) to two words of codes, with the group's
 // parameters; 4 neighbouring lanes hold the 64 values of a group.
 __device__ __forceinline__ void kv4_quantise(const uint32_t (&raw)[8], uint32_t (&word)[2], uint32_t& params) {
@@ -113,9 +163,10 @@ __device__ __forceinline__ void kv4_quantise(const uint32_t (&raw)[8], uint32_t 
   const uint64_t minus = f2_pack(-lo, -lo), times = f2_pack(r, r), magic = f2_pack(12582912.0f, 12582912.0f);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    // Adding 1.5 * 2^23 rounds the exact product to a whole number, ties to
-    // even, and leaves it (at most 15 (1 + 2^-8) before that) in the low bits
-    // of 0x4b400000; those constants add up to 0x4b400000 (16^8 - 1) / 15.
+    // Adding 1.5 * 2^23 rounds the exact product of the difference to a whole
+    // number, ties to even, and leaves it (at most 15 (1 + 2^-8) before that) in
+    // the low bits of 0x4b400000; those constants add up to 0x4b400000 (16^8 - 1)
+    // / 15.
     uint32_t sum = 0;
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
@@ -128,6 +179,19 @@ __device__ __forceinline__ void kv4_quantise(const uint32_t (&raw)[8], uint32_t 
     }
     word[w] = live ? sum - 0x4b400000u * 0x11111111u : 0u;
   }
+  // The difference of two bf16 is exact in fp32 unless one is below 2^-14 of the
+  // other. Where that is the minimum, or where so small an x could lie next to a tie
+  // (it is within 2^-10 steps of 0), the codes are looked at again.
+  const float zero = -lo * r;  // 0's code before it is rounded
+  const bool small = lo != 0.f && fabsf(lo) < 0x1p-14f * range;
+  if (live && (small || fabsf(zero - rintf(zero)) > 0.5f - 0x1p-10f)) {
+    const uint4 x = make_uint4(raw[0], raw[1], raw[2], raw[3]), y = make_uint4(raw[4], raw[5], raw[6], raw[7]);
+    if (kv4_near_tie(x, y, lo, r)) {
+      const uint2 exact = kv4_words_wide(x, y, lo, r);
+      word[0] = exact.x;
+      word[1] = exact.y;
+    }
+  }
 }
 
 // 32 bytes that are read once.
@@ -139,11 +203,12 @@ __device__ __forceinline__ void load_stream32(const void* p, uint32_t (&x)[8]) {
 
 // A thread takes 16 dimensions of K and of V of one token and head: 32 bytes
 // in, two words out of each. 4 x 8192 tokens of 16 heads of 128 (343 MB in and
-// out, 52 us at the copy's rate): 65 us, 5.3 TB/s. Bound by the issue of its
-// instructions (72% of the slots) close behind the memory: 8 dimensions a thread
-// took 105 us, unpacked arithmetic and two divisions a group 69.
+// out, 52 us at the copy's rate): 63 us, 5.4 TB/s. Bound by the issue of its
+// instructions close behind the memory: the look at what fp32 differences leave
+// out costs 4 us of it; 8 dimensions a thread took 105 us, unpacked arithmetic and
+// two divisions a group 69.
 template <int DH, bool WIDE>
-__global__ void __launch_bounds__(KV4_THREADS) kv4_store_kernel(const __grid_constant__ Kv4StoreArgs a) {
+__global__ void __launch_bounds__(KV4_THREADS, 6) kv4_store_kernel(const __grid_constant__ Kv4StoreArgs a) {
   constexpr int U = DH / 16;
   using L = Kv4<DH>;
   grid_dependency_wait();

@@ -499,12 +499,13 @@ int bpt_rotary(int dtype, const void* q, long long bs_q, long long ld_q, const v
  * for b sequences, kv_heads key/value heads of dh (64 or 128) dimensions and
  * `capacity` tokens (a positive multiple of 64) each; 4.5 bits an element. Per
  * token, head and 64 dimensions: min, scale = bf16((max - min) / 15), code =
- * rint((x - min) / scale) with the reciprocal of scale rounded to fp32; an
- * element's value is min + scale * code. A group that holds an infinity or a
- * NaN (or spans more than fp32's range) reads back as NaN. How many tokens a
- * sequence holds is the caller's: int32 `lens` [b] in device memory. A length,
- * start or count there that points outside the cache is cut to it and recorded
- * as BPT_ERR_RANGE in the stream's status (bpt_stream_status).
+ * rint((x - min) / scale) with the reciprocal of scale rounded to fp32, the
+ * difference and the product exact; an element's value is min + scale * code. A
+ * group that holds an infinity or a NaN (or spans more than fp32's range) reads
+ * back as NaN. How many tokens a sequence holds is the caller's: int32 `lens`
+ * [b] in device memory. A length, start or count there that points outside the
+ * cache is cut to it and recorded as BPT_ERR_RANGE in the stream's status
+ * (bpt_stream_status).
  *
  * Errors of these calls: BPT_ERR_SHAPE, BPT_ERR_NULL, BPT_ERR_ALIGN (16 bytes;
  * int32 arrays 4; strides of bf16 rows a multiple of 8 elements; the workspace
