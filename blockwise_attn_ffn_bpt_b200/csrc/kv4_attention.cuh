@@ -713,9 +713,16 @@ inline int kva_smem(int dh, int cols) {
 // about 2 us a block. Device time of one call, direct against split: 4 segments
 // of 200 tokens (dh = 64) 4.6 against 8.2 us; 32 segments (dh = 128) of 1000
 // tokens 8.8 against 10.0, of 2000 tokens 12.1 against 10.1; 128 segments of 3000
-// tokens 15.4 against 18.1.
+// tokens 15.4 against 18.1. These are for caches that are full: the host knows the
+// capacity alone, and a block with a long sequence among short ones keeps the
+// others waiting. So a warp takes 4 blocks at most: 148 segments (dh = 128) of 3072
+// tokens 15.3 against 19.5 us, with lengths spread evenly 15.0 against 15.1,
+// with one full sequence of 37 14.6 against 10.5; of 8192 tokens, which would be 11
+// blocks, 33.8 against 36.1, 31.6 against 22.8 and 30.9 against 12.2.
+constexpr int KVA_DIRECT = 4;
 inline bool kva_direct(long long segments, int blocks, int warps) {
-  return segments <= KVA_MAX_SMS && (long long)blocks * (KVA_MAX_SMS - segments) * 10 <= 16LL * warps * KVA_MAX_SMS;
+  return segments <= KVA_MAX_SMS && blocks <= KVA_DIRECT * warps &&
+         (long long)blocks * (KVA_MAX_SMS - segments) * 10 <= 16LL * warps * KVA_MAX_SMS;
 }
 
 inline bool kva_set_attributes() {
