@@ -10,8 +10,9 @@
 // little because a token's rot / 2 angles serve all of its heads, queries and
 // keys: a block computes them once per token into shared memory. An angle is
 // taken in turns in fp64 (pos * f / 2 pi, less its nearest whole number), so
-// that positions in the millions keep fp32 accuracy in what is left; the sine
-// and cosine of the remainder are then fp32.
+// that positions in the millions keep fp32 accuracy in what is left. Sine and
+// cosine are fp32's of the remainder in fp32, plus the first order of what that
+// rounding leaves (up to 9e-8 rad), rounded once with the magnitude.
 #pragma once
 
 #include "ptx.cuh"
@@ -176,9 +177,12 @@ __global__ void __launch_bounds__(ROT_THREADS, ROT_BLOCKS) rotary_kernel(const _
       pos = a.pos64 ? static_cast<const long long*>(a.positions)[at] : static_cast<const int*>(a.positions)[at];
     }
     const double turns = (double)pos * a.turns[j];
+    const double part = turns - rint(turns);
+    const float turn = (float)part, rest = 6.2831853f * (float)(part - (double)turn);
     float sn, cs;
-    sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-    table[ti * pairs + rot_place<W>(j, pairs)] = make_float2(cs * a.magnitude, sn * a.sine);
+    sincospif(2.0f * turn, &sn, &cs);
+    table[ti * pairs + rot_place<W>(j, pairs)] =
+        make_float2(fmaf(cs, a.magnitude, -sn * rest * a.magnitude), fmaf(sn, a.sine, cs * rest * a.sine));
   }
   __syncthreads();
 
