@@ -3,6 +3,9 @@ Python binding that is C++ (csrc/binding.cpp, linked with it).
 
     python -m blockwise_attn_ffn_bpt_b200.build [--force] [--verbose]
 
+Without torch the library alone is built (python blockwise_attn_ffn_bpt_b200/build.py:
+the package itself imports torch).
+
 nvcc cross-compiles without a GPU. The library links the CUDA runtime
 statically and reaches the driver's tensor-map encoder through the runtime's
 driver entry-point query, so it needs no libcuda at link time.
@@ -12,6 +15,8 @@ from __future__ import annotations
 
 import argparse
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -24,6 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbpt.so")
 BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BUILT_FOR = os.path.join(PKG, "_binding.torch")  # the torch that BINDING was built against
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -47,7 +53,26 @@ def sources():
 
 
 def up_to_date() -> bool:
-    return _newer(LIB, sources()) and _newer(BINDING, binding_sources())
+    return _newer(LIB, sources()) and (installed_torch() is None or binding_up_to_date())
+
+
+def installed_torch():
+    """The installed torch, as a text that another one has not; None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "?"
+    return f"{version} {spec.origin}"
+
+
+def binding_up_to_date() -> bool:
+    if not _newer(BINDING, binding_sources()) or not os.path.exists(BUILT_FOR):
+        return False
+    with open(BUILT_FOR) as f:
+        return f.read() == installed_torch()
 
 
 def binding_sources():
@@ -77,12 +102,22 @@ def build_binding() -> str:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stdout + res.stderr}")
     os.replace(tmp, BINDING)
+    with open(BUILT_FOR, "w") as f:
+        f.write(installed_torch())
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+    if force or not _newer(LIB, sources()):
+        build_library(verbose)
+    if installed_torch() is None:
+        print("torch is not installed: the C library was built, the Python binding was not", file=sys.stderr)
+    elif force or not binding_up_to_date():
+        build_binding()
+    return LIB
+
+
+def build_library(verbose: bool = False) -> str:
     cu = [p for p in sources() if p.endswith(".cu")]
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *cu]
@@ -95,7 +130,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         f.write(" ".join(cmd) + "\n" + log)
     if verbose:
         print(log)
-    build_binding()
     return LIB
 
 
