@@ -48,10 +48,11 @@
 // The products are mma.sync's: its operands are made in registers, where the
 // codes are unpacked, while tcgen05 would take them from shared or tensor memory,
 // a write and a read of four times the cache's bytes more. They fill a quarter of
-// the tensor pipe's cycles.
+// the tensor pipe's cycles (28% with one query a head, 24% with 8, over 8 x 8191
+// tokens of 32 heads of 128).
 //
-// Measured: 8 contexts of 32768 tokens, 32 heads of 128 (1.2 GB) 181 us, 6.7 TB/s;
-// 16 of 4096 tokens (302 MB) 57 us, 46 us of it at the memory's rate, the others
+// Measured: 8 contexts of 32768 tokens, 32 heads of 128 (1.2 GB) 183 us, 6.6 TB/s;
+// 16 of 4096 tokens (302 MB) 55 us, 46 us of it at the memory's rate, the others
 // being the start (3 us until the first blocks arrive) and the end (warps that
 // finish one after another). What bounds it then is the memory; in calls without
 // pause also the 1 kW power cap.
@@ -715,8 +716,8 @@ inline int kva_smem(int dh, int cols) {
 // tokens 8.8 against 10.0, of 2000 tokens 12.1 against 10.1; 128 segments of 3000
 // tokens 15.4 against 18.1. These are for caches that are full: the host knows the
 // capacity alone, and a block with a long sequence among short ones keeps the
-// others waiting. So a warp takes 4 blocks at most: 148 segments (dh = 128) of 3072
-// tokens 15.3 against 19.5 us, with lengths spread evenly 15.0 against 15.1,
+// others waiting. So a warp takes 4 blocks at most: 148 segments (dh = 128) of just
+// those 48 15.3 against 19.5 us, with lengths spread evenly 15.0 against 15.1,
 // with one full sequence of 37 14.6 against 10.5; of 8192 tokens, which would be 11
 // blocks, 33.8 against 36.1, 31.6 against 22.8 and 30.9 against 12.2.
 constexpr int KVA_DIRECT = 4;
@@ -950,7 +951,8 @@ __global__ void __launch_bounds__(KVW_THREADS, Q > 2 ? 4 : 8) kv4_weights_kernel
 // Whether the blocks of <2, 2> are too few to hide the latency of a read, and the
 // queries many: <1, 8> then. Device time of the kernel with <2, 2> and <1, 8>: 18
 // blocks, 88 queries 24.1 and 9.8 us; 256 blocks, 8 queries 3.8 and 2.5; 864 blocks,
-// 22 queries 10.7 and 13.0; 472 blocks, 4 queries 4.4 and 5.6.
+// 22 queries 10.7 and 13.0; 472 blocks, 4 queries 4.4 and 5.6. The blocks are
+// counted by the capacity; those past a sequence's length end at once.
 inline bool kvw_few(long long rows, int capacity, int cols) {
   return cols >= 8 && rows * ((capacity + KVW_THREADS * 8 - 1) / (KVW_THREADS * 8)) <= KVA_MAX_SMS * 4;
 }

@@ -14,9 +14,11 @@
 // words of 32 bits; word u holds dimensions 8u .. 8u + 7, dimension 8u + i in
 // bits 4i .. 4i + 3, and its place in the row is chosen so that the attention's
 // shared-memory reads are wide and free of bank conflicts (kv4_k_place,
-// kv4_v_place). K words are rotated left by 3 bits: a nibble then lands in bits
-// 3 .. 6 of a 16-bit half, where it completes a bf16 of value 16 + code.
-// Parameters are two bf16: scale in the lower half of 32 bits, min in the upper.
+// kv4_v_place). K words are rotated left by 3 bits: three shifts (0, 5 and 12 bits
+// to the right) then take the four nibbles of every 16-bit half to bits 3 .. 6,
+// 2 .. 5, 6 .. 9 and 3 .. 6, within its 10 lowest bits, where one mask more leaves
+// a subnormal fp16 number (kv4_attention.cuh). Parameters are two bf16: scale in
+// the lower half of 32 bits, min in the upper.
 #pragma once
 
 #include "ptx.cuh"
@@ -204,7 +206,7 @@ __device__ __forceinline__ void load_stream32(const void* p, uint32_t (&x)[8]) {
 // A thread takes 16 dimensions of K and of V of one token and head: 32 bytes
 // in, two words out of each. 4 x 8192 tokens of 16 heads of 128 (343 MB in and
 // out, 52 us at the copy's rate): 63 us, 5.4 TB/s. Bound by the issue of its
-// instructions close behind the memory: the look at what fp32 differences leave
+// instructions (80% of the slots) close behind the memory: the look at what fp32 differences leave
 // out costs 4 us of it; 8 dimensions a thread took 105 us, unpacked arithmetic and
 // two divisions a group 69.
 template <int DH, bool WIDE>

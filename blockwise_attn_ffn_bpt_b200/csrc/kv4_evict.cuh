@@ -261,7 +261,10 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(const __grid_consta
 // Blocks of a cluster: more where a row is long and the rows alone leave SMs
 // idle (two blocks on an SM gain nothing). Device time, 1 against 2 and 4 blocks:
 // 4 rows of 8192 tokens 11.3, 12.4, 12.3 us, of 32768 tokens 18.8, 15.8, 14.8, 2
-// rows of 131072 tokens 69, 42, 22; 64 rows of 32768 tokens 23.9, 20.0, 30.7.
+// rows of 131072 tokens 69, 42, 22; 64 rows of 32768 tokens 23.9, 20.0, 30.7. That
+// is with full rows; the host knows the capacity alone, and the rows may be short:
+// an eviction from 64 rows of 4096 tokens takes 9.0 us with that capacity (one
+// block), 12.4 with 32768 (two).
 inline int evict_cluster(long long rows, int capacity) {
   if (capacity < 16384) return 1;
   return rows * 4 <= KVA_MAX_SMS ? 4 : rows * 2 <= KVA_MAX_SMS ? 2 : 1;
@@ -270,7 +273,9 @@ inline int evict_cluster(long long rows, int capacity) {
 // Threads of a block: few where the rows, two blocks of 1024 an SM, would take a
 // second round, and are short. Device time of the selection, 1024 against 256: 1440
 // rows of 512 tokens 42.6, 20.4 us; 1024 of 2048 34.4, 22.2, of 4096 38.6, 28.8; 296
-// of 4096 12.3, 13.2; 64 of 2048 5.3, 6.7.
+// of 4096 12.3, 13.2; 64 of 2048 5.3, 6.7. As above with full rows: an eviction
+// from 1440 rows of 512 takes 29 us with a capacity of 512 or 4096 (256 threads),
+// 50 with 32768 (1024).
 inline int evict_threads(int cl, long long rows, int capacity) {
   return cl == 1 && rows > KVA_MAX_SMS * 2 && capacity <= 4096 ? EVICT_SHORT : EVICT_THREADS;
 }

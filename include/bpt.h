@@ -548,7 +548,9 @@ int bpt_kv4_load(const void* cache, int b, int kv_heads, int capacity, int dh, c
  * that is more, is lost. V is below 2^96: weights of up to 2^8 are summed over
  * the tokens before the division.
  * workspace: bpt_kv4_attention_workspace_bytes of the same arguments, which may
- * be 0 (short caches without weights; workspace may then be NULL). */
+ * be 0 (short caches without weights; workspace may then be NULL). With weights
+ * it holds the scores, 4 bytes for each of the b n heads queries and `capacity`
+ * places, whatever the lengths. */
 size_t bpt_kv4_attention_workspace_bytes(int b, int n, int heads, int kv_heads, int capacity, int dh,
                                          int with_weights);
 int bpt_kv4_attention(const void* q, long long bs_q, long long ld_q, const void* cache, const int* lens, int b,
